@@ -65,6 +65,8 @@ extern "C" {
 #define MOEQ_MAX_TOPK 16
 #define MOEQ_MAX_HIDDEN 8192
 #define MOEQ_MAX_INTER 8192
+#define MOEQ_MAX_GROUPS 16384 /* groups of a grouped product */
+#define MOEQ_MAX_WIDTH 65536  /* matrix sides of the linear, grouped and SwiGLU entry points */
 
 typedef enum {
     MOE_OK = 0,
@@ -81,6 +83,9 @@ typedef enum {
     MOE_FMT_AFFINE_INT8 = 1,
     MOE_FMT_MIXED_TERNARY_INT4 = 2
 } moe_format;
+
+/* Element types of the grouped products and of SwiGLU. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype;
 
 typedef void* moe_stream; /* cudaStream_t */
 
@@ -455,6 +460,78 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
                                              const moe_mixed_tensor* down, const uint16_t* x, int32_t T,
                                              int32_t residual, float eps, uint16_t* y, void* workspace,
                                              size_t ws_bytes, moe_stream stream);
+
+/* --------------------------------------------- linear layers in the affine format
+ * The other linear layers of a packed checkpoint: the d1a MLX port keeps 276 layers as
+ * int4 groups ("4-bit 分组量化"), the Edge0 gates are int8 ("Recover-LoRA" page, section 一).
+ *  moe_affine_linear:    y[t][n] = sum_k (s q + b)[n][k] x[t][k]
+ *  moe_affine_linear_dx: dx[t][k] = sum_n dy[t][n] (s q + b)[n][k], the gradient of x through
+ *    the frozen packed weights (adapter training over the int4 base, section 二 of that page).
+ * W: one matrix (n = 1) of either affine format, any `out`, group a multiple of 32 that divides
+ * `in`, packed words 16-byte aligned; out, in <= MOEQ_MAX_WIDTH or MOE_ERR_UNSUPPORTED (out: up to
+ * 1 << 24).  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out]; outputs may
+ * not alias inputs.  fp32 accumulation.  The codes enter the forward's sums as whole numbers, s and b once
+ * per group; dx first writes the matrix into the workspace as bf16 (one rounding per weight, at most
+ * 2^-8 of it) and multiplies that.  An infinite
+ * or NaN input makes the outputs that depend on it infinite or NaN.
+ * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses),
+ * 256-byte aligned, initialised once with moe_workspace_init; it holds the status word, and
+ * nothing else outlives a call.  T = 0 enqueues nothing. */
+MOEQ_API size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T);
+MOEQ_API moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y,
+                                      void* workspace, size_t ws_bytes, moe_stream stream);
+MOEQ_API size_t moe_affine_linear_dx_workspace_bytes(const moe_qtensor* W, int32_t T);
+MOEQ_API moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* dy, int32_t T, uint16_t* dx,
+                                         void* workspace, size_t ws_bytes, moe_stream stream);
+
+/* ------------------------------------------------------ products grouped by expert
+ * Unpacked matrices W [G][N][K] (one per group, row-major as everywhere: N outputs, K inputs) and
+ * rows sorted by group: group g owns rows [offsets[g], offsets[g+1]), any number of them, none
+ * included.  No counterpart on the pages, which only run packed experts: these are the products an
+ * unquantised expert layer and the training of adapter factors (a group per expert, or per expert
+ * and adapter) are made of, next to moe_index_build, whose `offsets` they take, and
+ * moe_ep_dispatch.
+ *  moe_grouped_matmul:    y[m][n]     = sum_k x[m][k] W[g][n][k]      x [M][K], y [M][N]
+ *  moe_grouped_matmul_dx: dx[m][k]    = sum_n dy[m][n] W[g][n][k]     dy [M][N], dx [M][K]
+ *  moe_grouped_matmul_dw: dw[g][n][k] = sum_m dy[m][n] x[m][k]        dw [G][N][K]
+ * All pointers device memory.  dtype: MOE_DT_BF16 or MOE_DT_F16, of x, dy, W and the output; dw may
+ * also be MOE_DT_F32 (out_dtype).  fp32 accumulation, one rounding at the end.  accumulate = 1: dw
+ * holds earlier gradients and the sums are added to them (in fp32, rounded once); 0: dw is
+ * overwritten, with zeros for a group without rows.
+ *  offsets device int32 [G+1], non-decreasing within [0, M]; NULL with G = 1: one group of all M
+ *          rows.  Rows outside [offsets[0], offsets[G]) are neither read into any result nor
+ *          written.  Offsets that break the rule raise MOE_ERR_DEVICE_INDEX in *status; they are
+ *          clamped to [0, M] and to the largest one before them, so that nothing out of range is
+ *          touched.
+ *  status  device int32 word, zeroed by the caller: MOE_ERR_DEVICE_INDEX, or MOE_ERR_TIMEOUT
+ *          when a bounded wait ran out (the output is then incomplete).
+ * Any N and K up to MOEQ_MAX_WIDTH, G up to MOEQ_MAX_GROUPS (MOE_ERR_UNSUPPORTED beyond).  Results do not depend on the other groups' rows or, run to run, on
+ * scheduling.  Outputs may not alias inputs.  M = 0 enqueues nothing but dw's zeros. */
+MOEQ_API moe_status moe_grouped_matmul(int32_t dtype, const void* x, const int32_t* offsets, const void* W, int32_t M,
+                                       int32_t G, int32_t N, int32_t K, void* y, int32_t* status, moe_stream stream);
+MOEQ_API moe_status moe_grouped_matmul_dx(int32_t dtype, const void* dy, const int32_t* offsets, const void* W,
+                                          int32_t M, int32_t G, int32_t N, int32_t K, void* dx, int32_t* status,
+                                          moe_stream stream);
+MOEQ_API moe_status moe_grouped_matmul_dw(int32_t dtype, const void* dy, const void* x, const int32_t* offsets,
+                                          int32_t M, int32_t G, int32_t N, int32_t K, int32_t out_dtype,
+                                          int32_t accumulate, void* dw, int32_t* status, moe_stream stream);
+
+/* ------------------------------------------------------------ SwiGLU on rows
+ * Between an expert's two products, on stacked rows gu = [gate | up] [M][2I], with a weight per
+ * row (the routing weight: W_d (w h) = w W_d h, so the combine is then a plain sum and the weight
+ * gets its gradient here):
+ *  moe_swiglu:      h[m][i] = w[m] silu(gate[m][i]) up[m][i]
+ *  moe_swiglu_grad: dgu = [w dh up silu'(gate) | w dh silu(gate)] and
+ *                   dw[m] = sum_i dh silu(gate) up, for the gradient dh of h
+ * (SiLU on the gate branch, as in moe_ffn_forward.)  dtype: MOE_DT_BF16 or MOE_DT_F16, of gu, h, dh
+ * and dgu; w, dw fp32 [M]; w NULL: 1; dw NULL: not wanted.  Rows [offsets[0], offsets[G]) of the
+ * G + 1 offsets on the device (clamped to [0, M]); offsets NULL: all M.  Other rows are neither read
+ * nor written.  fp32 arithmetic, one rounding.  I <= MOEQ_MAX_WIDTH.  Outputs may not alias inputs. */
+MOEQ_API moe_status moe_swiglu(int32_t dtype, const void* gu, const float* w, const int32_t* offsets, int32_t G,
+                               int32_t M, int32_t I, void* h, moe_stream stream);
+MOEQ_API moe_status moe_swiglu_grad(int32_t dtype, const void* gu, const float* w, const void* dh,
+                                    const int32_t* offsets, int32_t G, int32_t M, int32_t I, void* dgu, float* dw,
+                                    moe_stream stream);
 
 /* ---------------------------------------------------------- kernel timing
  * Opt-in measurement of the library's own kernels with CUDA events (no device

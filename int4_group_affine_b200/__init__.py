@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import (FMT_AFFINE_INT4, FMT_AFFINE_INT8, FMT_MIXED_TERNARY_INT4, Layer, LoraProj, LoraPtrs,
+from ._lib import (DT_BF16, DT_F16, DT_F32, FMT_AFFINE_INT4, FMT_AFFINE_INT8, FMT_MIXED_TERNARY_INT4, Layer, LoraProj, LoraPtrs,
                    MixedTensor, Prerouter, QTensor, STATUS_NAMES)
 
 __all__ = [
@@ -26,6 +26,9 @@ __all__ = [
     "moe_mixed_linear_a8_workspace_bytes", "moe_mixed_linear_a8", "moe_mixed_mlp_a8_workspace_bytes",
     "moe_mixed_mlp_forward_a8", "moe_experts_workspace_bytes", "moe_experts_forward", "moe_ep_dispatch",
     "moe_ep_combine", "moe_ffn_forward_host", "moe_set_decode_path", "moe_decode_path", "DECODE_AUTO", "DECODE_CHAIN", "DECODE_BARRIER", "DECODE_CLUSTER",
+    "DT_BF16", "DT_F16", "DT_F32", "moe_affine_linear_workspace_bytes", "moe_affine_linear",
+    "moe_affine_linear_dx_workspace_bytes", "moe_affine_linear_dx", "moe_grouped_matmul", "moe_grouped_matmul_dx",
+    "moe_grouped_matmul_dw", "moe_swiglu", "moe_swiglu_grad",
 ]
 
 DECODE_AUTO, DECODE_CHAIN, DECODE_BARRIER, DECODE_CLUSTER = 0, 1, 2, 3
@@ -292,3 +295,69 @@ def moe_set_decode_path(path: int):
 
 def moe_decode_path() -> int:
     return int(_lib.lib().moe_decode_path())
+
+
+def _here(*tensors):
+    """Addresses of tensors of the current device (or raw addresses): the library enqueues on the current
+    device, where another device's memory is not its own."""
+    import torch
+    cur = torch.cuda.current_device() if any(hasattr(t, "is_cuda") for t in tensors) else None
+    for t in tensors:
+        if hasattr(t, "is_cuda") and t.is_cuda and t.device.index != cur:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, cur))
+    return [_ptr(t) for t in tensors]
+
+
+def moe_affine_linear_workspace_bytes(W: QTensor, T) -> int:
+    return int(_lib.lib().moe_affine_linear_workspace_bytes(ctypes.byref(W), T))
+
+
+def moe_affine_linear(W: QTensor, x, T, y, workspace, ws_bytes, stream=None):
+    """y = x times the packed matrix (bf16 rows [T, in] -> [T, out])."""
+    px, py, pw = _here(x, y, workspace)
+    _check("moe_affine_linear", _lib.lib().moe_affine_linear(ctypes.byref(W), px, T, py, pw, ws_bytes,
+                                                             _stream(stream)))
+
+
+def moe_affine_linear_dx_workspace_bytes(W: QTensor, T) -> int:
+    return int(_lib.lib().moe_affine_linear_dx_workspace_bytes(ctypes.byref(W), T))
+
+
+def moe_affine_linear_dx(W: QTensor, dy, T, dx, workspace, ws_bytes, stream=None):
+    """dx, the gradient of moe_affine_linear's x for the gradient dy of its y."""
+    py, px, pw = _here(dy, dx, workspace)
+    _check("moe_affine_linear_dx", _lib.lib().moe_affine_linear_dx(ctypes.byref(W), py, T, px, pw, ws_bytes,
+                                                                   _stream(stream)))
+
+
+def moe_grouped_matmul(dtype, x, offsets, W, M, G, N, K, y, status, stream=None):
+    """y[m] = W[g] x[m] for the rows of each group g (dtype DT_BF16 or DT_F16)."""
+    px, po, pw, py, ps = _here(x, offsets, W, y, status)
+    _check("moe_grouped_matmul", _lib.lib().moe_grouped_matmul(dtype, px, po, pw, M, G, N, K, py, ps,
+                                                               _stream(stream)))
+
+
+def moe_grouped_matmul_dx(dtype, dy, offsets, W, M, G, N, K, dx, status, stream=None):
+    """dx[m] = W[g]^T dy[m], the gradient of moe_grouped_matmul's x."""
+    py, po, pw, px, ps = _here(dy, offsets, W, dx, status)
+    _check("moe_grouped_matmul_dx", _lib.lib().moe_grouped_matmul_dx(dtype, py, po, pw, M, G, N, K, px, ps,
+                                                                     _stream(stream)))
+
+
+def moe_grouped_matmul_dw(dtype, dy, x, offsets, M, G, N, K, out_dtype, accumulate, dw, status, stream=None):
+    """dw[g] (+)= sum over the rows of group g of dy[m] x[m]^T, the gradient of moe_grouped_matmul's W."""
+    py, px, po, pw, ps = _here(dy, x, offsets, dw, status)
+    _check("moe_grouped_matmul_dw", _lib.lib().moe_grouped_matmul_dw(
+        dtype, py, px, po, M, G, N, K, out_dtype, int(accumulate), pw, ps, _stream(stream)))
+
+
+def moe_swiglu(dtype, gu, w, offsets, G, M, I, h, stream=None):
+    """h = w * silu(gate) * up of stacked rows gu = [gate | up] ([M, 2 I])."""
+    pg, pw, po, ph = _here(gu, w, offsets, h)
+    _check("moe_swiglu", _lib.lib().moe_swiglu(dtype, pg, pw, po, G, M, I, ph, _stream(stream)))
+
+
+def moe_swiglu_grad(dtype, gu, w, dh, offsets, G, M, I, dgu, dw, stream=None):
+    """The gradients of moe_swiglu's gu and w (dw None: not wanted) for the gradient dh of its h."""
+    pg, pw, pd, po, pu, px = _here(gu, w, dh, offsets, dgu, dw)
+    _check("moe_swiglu_grad", _lib.lib().moe_swiglu_grad(dtype, pg, pw, pd, po, G, M, I, pu, px, _stream(stream)))

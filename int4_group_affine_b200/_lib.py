@@ -17,6 +17,7 @@ MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
                 4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_DEVICE_INDEX", 6: "MOE_ERR_TIMEOUT"}
 FMT_AFFINE_INT4, FMT_AFFINE_INT8, FMT_MIXED_TERNARY_INT4 = 0, 1, 2
+DT_BF16, DT_F16, DT_F32 = 0, 1, 2
 
 # Every function the header declares, with (restype, argtypes).
 P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -95,6 +96,15 @@ SIGNATURES = {
     "moe_experts_forward": (ctypes.c_int, [PL, P, P, P, I32, P, P, SZ, P]),
     "moe_ep_dispatch": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
     "moe_ep_combine": (ctypes.c_int, [P, P, P, P, P, I32, I32, I32, P, P]),
+    "moe_affine_linear_workspace_bytes": (SZ, [PQ, I32]),
+    "moe_affine_linear": (ctypes.c_int, [PQ, P, I32, P, P, SZ, P]),
+    "moe_affine_linear_dx_workspace_bytes": (SZ, [PQ, I32]),
+    "moe_affine_linear_dx": (ctypes.c_int, [PQ, P, I32, P, P, SZ, P]),
+    "moe_grouped_matmul": (ctypes.c_int, [I32, P, P, P, I32, I32, I32, I32, P, P, P]),
+    "moe_grouped_matmul_dx": (ctypes.c_int, [I32, P, P, P, I32, I32, I32, I32, P, P, P]),
+    "moe_grouped_matmul_dw": (ctypes.c_int, [I32, P, P, P, I32, I32, I32, I32, I32, I32, P, P, P]),
+    "moe_swiglu": (ctypes.c_int, [I32, P, P, P, I32, I32, I32, P, P]),
+    "moe_swiglu_grad": (ctypes.c_int, [I32, P, P, P, P, I32, I32, I32, P, P, P]),
     "moe_timing_kinds": (ctypes.c_int, []),
     "moe_timing_kind_name": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_timing_enable": (ctypes.c_int, [ctypes.c_int]),

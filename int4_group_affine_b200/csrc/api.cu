@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "grouped.cuh"
 
 namespace moeq {
 
@@ -911,6 +912,195 @@ moe_status moe_ep_combine(const uint16_t* ret, const int32_t* pos, const float* 
     cudaStream_t s = (cudaStream_t)stream;
     timing_begin(s);
     LAUNCH(kEpCombine, launch_ep_combine(ret, pos, topk_w, shared, shared_scale, T, K, H, y, s));
+    return MOE_OK;
+}
+
+// ------------------------------------------------- linear layers in the affine format
+namespace {
+constexpr int kMaxLinearOut = 1 << 24;
+
+// The matrix of a linear call: MOE_OK, or the status it is refused with.
+moe_status linear_check(const moe_qtensor* W) {
+    if (!W || W->out <= 0 || W->in <= 0 || (W->bits != 4 && W->bits != 8)) return MOE_ERR_INVALID_ARG;
+    if (!qtensor_ok(*W, 1, W->out, W->in, W->bits)) return MOE_ERR_INVALID_ARG;
+    if (W->out > kMaxLinearOut || W->in > MOEQ_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// status word, then the matrix as bf16 where the call multiplies that
+size_t linear_bytes(const moe_qtensor* W, bool matrix) {
+    return kAlign + (matrix ? align_up((size_t)W->out * W->in * 2) : 0);
+}
+
+// One group of T rows on the matrix in the workspace.
+GmmArgs linear_gmm(const moe_qtensor* W, const uint16_t* rows, int T, uint16_t* out, void* ws) {
+    GmmArgs a;
+    memset(&a, 0, sizeof(a));
+    a.a = rows;
+    a.b = (const uint16_t*)((char*)ws + kAlign);
+    a.out = out;
+    a.M = T;
+    a.G = 1;
+    a.N = W->out;
+    a.K = W->in;
+    a.status = (int32_t*)ws;
+    a.wait_ns = wait_limit_ns();
+    return a;
+}
+}  // namespace
+
+size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T) {
+    if (T < 0 || linear_check(W) != MOE_OK) return 0;
+    return linear_bytes(W, false);
+}
+
+moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y, void* workspace,
+                             size_t ws_bytes, moe_stream stream) {
+    moe_status st = linear_check(W);
+    if (st != MOE_OK) return st;
+    CHECK_ARG(T >= 0);
+    st = ws_check(workspace, ws_bytes, moe_affine_linear_workspace_bytes(W, T));
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    CHECK_ARG(x && y && x != y && aligned(x, 16) && aligned(y, 2));
+    cudaStream_t s = (cudaStream_t)stream;
+    timing_begin(s);
+    LAUNCH(kAffineLinear, launch_affine_linear(*W, x, T, y, s));
+    return MOE_OK;
+}
+
+size_t moe_affine_linear_dx_workspace_bytes(const moe_qtensor* W, int32_t T) {
+    if (T < 0 || linear_check(W) != MOE_OK) return 0;
+    return linear_bytes(W, true);
+}
+
+moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* dy, int32_t T, uint16_t* dx, void* workspace,
+                                size_t ws_bytes, moe_stream stream) {
+    moe_status st = linear_check(W);
+    if (st != MOE_OK) return st;
+    CHECK_ARG(T >= 0);
+    st = ws_check(workspace, ws_bytes, linear_bytes(W, true));
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    CHECK_ARG(dy && dx && dy != dx && aligned(dx, 16) && aligned(dy, 2));
+    cudaStream_t s = (cudaStream_t)stream;
+    timing_begin(s);
+    LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)((char*)workspace + kAlign), s));
+    LAUNCH(kGroupedDx, launch_grouped(kGmmDx, 0, linear_gmm(W, dy, T, dx, workspace), s));
+    return MOE_OK;
+}
+
+// ------------------------------------------------------- products grouped by expert
+namespace {
+moe_status grouped_check(int32_t dtype, const int32_t* offsets, int32_t M, int32_t G, int32_t N, int32_t K,
+                         const int32_t* status) {
+    CHECK_ARG(dtype == MOE_DT_BF16 || dtype == MOE_DT_F16 || dtype == MOE_DT_F32);
+    CHECK_ARG(M >= 0 && G > 0 && N > 0 && K > 0 && (offsets || G == 1) && status);
+    CHECK_ARG(aligned(offsets, 4) && aligned(status, 4));
+    if (dtype == MOE_DT_F32 || G > MOEQ_MAX_GROUPS || N > MOEQ_MAX_WIDTH || K > MOEQ_MAX_WIDTH)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+GmmArgs gmm_args(const void* a, const void* b, const int32_t* offsets, int M, int G, int N, int K, void* out,
+                 int32_t* status) {
+    GmmArgs r;
+    memset(&r, 0, sizeof(r));
+    r.a = (const uint16_t*)a;
+    r.b = (const uint16_t*)b;
+    r.off = offsets;
+    r.out = out;
+    r.M = M;
+    r.G = G;
+    r.N = N;
+    r.K = K;
+    r.status = status;
+    r.wait_ns = wait_limit_ns();
+    return r;
+}
+}  // namespace
+
+moe_status moe_grouped_matmul(int32_t dtype, const void* x, const int32_t* offsets, const void* W, int32_t M,
+                              int32_t G, int32_t N, int32_t K, void* y, int32_t* status, moe_stream stream) {
+    moe_status st = grouped_check(dtype, offsets, M, G, N, K, status);
+    if (st != MOE_OK) return st;
+    if (M == 0) return MOE_OK;
+    CHECK_ARG(x && W && y && y != x && y != W && aligned(x, 2) && aligned(W, 2) && aligned(y, 2));
+    cudaStream_t s = (cudaStream_t)stream;
+    timing_begin(s);
+    LAUNCH(kGroupedFwd, launch_grouped(kGmmFwd, dtype == MOE_DT_F16, gmm_args(x, W, offsets, M, G, N, K, y, status), s));
+    return MOE_OK;
+}
+
+moe_status moe_grouped_matmul_dx(int32_t dtype, const void* dy, const int32_t* offsets, const void* W, int32_t M,
+                                 int32_t G, int32_t N, int32_t K, void* dx, int32_t* status, moe_stream stream) {
+    moe_status st = grouped_check(dtype, offsets, M, G, N, K, status);
+    if (st != MOE_OK) return st;
+    if (M == 0) return MOE_OK;
+    CHECK_ARG(dy && W && dx && dx != dy && dx != W && aligned(dy, 2) && aligned(W, 2) && aligned(dx, 2));
+    cudaStream_t s = (cudaStream_t)stream;
+    timing_begin(s);
+    LAUNCH(kGroupedDx,
+           launch_grouped(kGmmDx, dtype == MOE_DT_F16, gmm_args(dy, W, offsets, M, G, N, K, dx, status), s));
+    return MOE_OK;
+}
+
+moe_status moe_grouped_matmul_dw(int32_t dtype, const void* dy, const void* x, const int32_t* offsets, int32_t M,
+                                 int32_t G, int32_t N, int32_t K, int32_t out_dtype, int32_t accumulate, void* dw,
+                                 int32_t* status, moe_stream stream) {
+    moe_status st = grouped_check(dtype, offsets, M, G, N, K, status);
+    if (st != MOE_OK) return st;
+    CHECK_ARG((out_dtype == dtype || out_dtype == MOE_DT_F32) && (accumulate == 0 || accumulate == 1));
+    CHECK_ARG(dw && aligned(dw, out_dtype == MOE_DT_F32 ? 4 : 2));
+    if (M == 0 && accumulate) return MOE_OK;
+    if (M > 0) CHECK_ARG(dy && x && dw != dy && dw != x && aligned(dy, 2) && aligned(x, 2));
+    cudaStream_t s = (cudaStream_t)stream;
+    GmmArgs a = gmm_args(dy, x, M == 0 ? nullptr : offsets, M, G, N, K, dw, status);
+    a.out_f32 = out_dtype == MOE_DT_F32;
+    a.accumulate = accumulate;
+    timing_begin(s);
+    if (M == 0) {
+        CHECK_CUDA(cudaMemsetAsync(dw, 0, (size_t)G * N * K * (a.out_f32 ? 4 : 2), s));
+        return MOE_OK;
+    }
+    LAUNCH(kGroupedDw, launch_grouped(kGmmDw, dtype == MOE_DT_F16, a, s));
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------ SwiGLU on rows
+namespace {
+moe_status swiglu_check(int32_t dtype, const float* w, const int32_t* offsets, int32_t G, int32_t M, int32_t I) {
+    CHECK_ARG(dtype == MOE_DT_BF16 || dtype == MOE_DT_F16 || dtype == MOE_DT_F32);
+    CHECK_ARG(M >= 0 && I > 0 && (!offsets || G > 0) && aligned(w, 4) && aligned(offsets, 4));
+    if (dtype == MOE_DT_F32 || I > MOEQ_MAX_WIDTH || (offsets && G > MOEQ_MAX_GROUPS)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_swiglu(int32_t dtype, const void* gu, const float* w, const int32_t* offsets, int32_t G, int32_t M,
+                      int32_t I, void* h, moe_stream stream) {
+    moe_status st = swiglu_check(dtype, w, offsets, G, M, I);
+    if (st != MOE_OK) return st;
+    if (M == 0) return MOE_OK;
+    CHECK_ARG(gu && h && gu != h && aligned(gu, 2) && aligned(h, 2));
+    cudaStream_t s = (cudaStream_t)stream;
+    const SwigluArgs a{(const uint16_t*)gu, w, nullptr, offsets, G, M, I, (uint16_t*)h, nullptr, nullptr};
+    timing_begin(s);
+    LAUNCH(kSwiglu, launch_swiglu(dtype == MOE_DT_F16, 0, a, s));
+    return MOE_OK;
+}
+
+moe_status moe_swiglu_grad(int32_t dtype, const void* gu, const float* w, const void* dh, const int32_t* offsets,
+                           int32_t G, int32_t M, int32_t I, void* dgu, float* dw, moe_stream stream) {
+    moe_status st = swiglu_check(dtype, w, offsets, G, M, I);
+    if (st != MOE_OK) return st;
+    if (M == 0) return MOE_OK;
+    CHECK_ARG(gu && dh && dgu && dgu != gu && dgu != dh && (!dw || dw != w));
+    CHECK_ARG(aligned(gu, 2) && aligned(dh, 2) && aligned(dgu, 2) && aligned(dw, 4));
+    cudaStream_t s = (cudaStream_t)stream;
+    const SwigluArgs a{(const uint16_t*)gu, w, (const uint16_t*)dh, offsets, G, M, I, nullptr, (uint16_t*)dgu, dw};
+    timing_begin(s);
+    LAUNCH(kSwigluGrad, launch_swiglu(dtype == MOE_DT_F16, 1, a, s));
     return MOE_OK;
 }
 

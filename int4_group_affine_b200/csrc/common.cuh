@@ -145,7 +145,8 @@ struct DecodeScratch {
 enum Kind {
     kPack, kDequant, kRouter, kTopk, kIndexCount, kIndexScan, kIndexScatter, kLoraA, kGateUp, kDown,
     kCombine, kRmsnorm, kMixedGateUp, kMixedDown, kMixedLinear, kDecode, kTcLoraGUKind, kTcGUKind,
-    kTcLoraDownKind, kTcDownKind, kTcRouterKind, kKpermKind, kDecodeChain, kPrerouter, kAct8, kMixedA8, kEpDispatch, kEpCombine, kDecodeCluster, kKindCount
+    kTcLoraDownKind, kTcDownKind, kTcRouterKind, kKpermKind, kDecodeChain, kPrerouter, kAct8, kMixedA8, kEpDispatch, kEpCombine, kDecodeCluster,
+    kAffineLinear, kAffineDequant, kGroupedFwd, kGroupedDx, kGroupedDw, kSwiglu, kSwigluGrad, kKindCount
 };
 void timing_begin(cudaStream_t s);
 void timing_mark(int kind, cudaStream_t s);
@@ -264,6 +265,27 @@ cudaError_t launch_ep_dispatch(const uint16_t* x, const int32_t* idx, const int3
                                int32_t* meta, int32_t* status, cudaStream_t s);
 cudaError_t launch_ep_combine(const uint16_t* ret, const int32_t* pos, const float* w, const uint16_t* shared,
                               const float* sg, int T, int K, int H, uint16_t* y, cudaStream_t s);
+
+// Rows times an affine-packed matrix (csrc/linear.cu): y bf16 [T][out]; the matrix as bf16 [out][in].
+cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T, uint16_t* y, cudaStream_t s);
+cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s);
+
+// Products grouped by expert (csrc/grouped.cu; arguments in grouped.cuh).
+struct GmmArgs;
+cudaError_t launch_grouped(int dir, int f16, const GmmArgs& a, cudaStream_t s);
+
+// SwiGLU of stacked [gate | up] rows and its gradient (csrc/swiglu.cu): rows [off[0], off[G]).
+struct SwigluArgs {
+    const uint16_t* gu;  // [M][2I]
+    const float* w;      // [M] or NULL
+    const uint16_t* dh;  // [M][I] (gradient)
+    const int32_t* off;  // device [G+1] or NULL (all M rows)
+    int G, M, I;
+    uint16_t* h;         // [M][I]
+    uint16_t* dgu;       // [M][2I] (gradient)
+    float* dw;           // [M] (gradient) or NULL
+};
+cudaError_t launch_swiglu(int f16, int grad, const SwigluArgs& a, cudaStream_t s);
 
 // Device row offset (in words) of row `o` of a mixed matrix with super-group size G.
 __host__ __device__ __forceinline__ int64_t mixed_row_offset(int o, int in, int G) {
