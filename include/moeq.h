@@ -505,7 +505,9 @@ MOEQ_API moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* d
  *          touched.
  *  status  device int32 word, zeroed by the caller: MOE_ERR_DEVICE_INDEX, or MOE_ERR_TIMEOUT
  *          when a bounded wait ran out (the output is then incomplete).
- * Any N and K up to MOEQ_MAX_WIDTH, G up to MOEQ_MAX_GROUPS (MOE_ERR_UNSUPPORTED beyond).  Results do not depend on the other groups' rows or, run to run, on
+ * Any N and K up to MOEQ_MAX_WIDTH, G up to MOEQ_MAX_GROUPS (MOE_ERR_UNSUPPORTED beyond).  Operands that
+ * start on 16 bytes and whose rows (x, dy, W; dw) are multiples of 16 bytes run on the tcgen05
+ * kernel, others on warp-level tiles.  Results do not depend on the other groups' rows or, run to run, on
  * scheduling.  Outputs may not alias inputs.  M = 0 enqueues nothing but dw's zeros. */
 MOEQ_API moe_status moe_grouped_matmul(int32_t dtype, const void* x, const int32_t* offsets, const void* W, int32_t M,
                                        int32_t G, int32_t N, int32_t K, void* y, int32_t* status, moe_stream stream);

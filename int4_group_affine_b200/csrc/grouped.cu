@@ -182,6 +182,7 @@ cudaError_t launch_any(const GmmArgs& a, int f16, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_grouped(int dir, int f16, const GmmArgs& a, cudaStream_t s) {
+    if (grouped_tc_supported(dir, a)) return launch_grouped_tc(dir, f16, a, s);
     switch (dir) {
         case kGmmFwd: return launch_any<kGmmFwd>(a, f16, s);
         case kGmmDx: return launch_any<kGmmDx>(a, f16, s);

@@ -24,6 +24,10 @@ struct GmmArgs {
     uint64_t wait_ns;
 };
 
+// The tcgen05 kernel (grouped_tc.cu), and whether it takes these operands.
+bool grouped_tc_supported(int dir, const GmmArgs& a);
+cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s);
+
 // A group's rows.  The device sees the offsets for the first time, so whatever they hold no row
 // may be touched out of range or by two groups: they are clamped to [0, M] and a running maximum
 // makes them non-decreasing (which changes nothing for a proper prefix sum).
