@@ -918,6 +918,7 @@ moe_status moe_ep_combine(const uint16_t* ret, const int32_t* pos, const float* 
 // ------------------------------------------------- linear layers in the affine format
 namespace {
 constexpr int kMaxLinearOut = 1 << 24;
+constexpr int kLinearMatrixRows = 65;  // from this many rows on, the matrix in bf16 is multiplied
 
 // The matrix of a linear call: MOE_OK, or the status it is refused with.
 moe_status linear_check(const moe_qtensor* W) {
@@ -951,7 +952,7 @@ GmmArgs linear_gmm(const moe_qtensor* W, const uint16_t* rows, int T, uint16_t* 
 
 size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T) {
     if (T < 0 || linear_check(W) != MOE_OK) return 0;
-    return linear_bytes(W, false);
+    return linear_bytes(W, T >= kLinearMatrixRows);
 }
 
 moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y, void* workspace,
@@ -965,6 +966,11 @@ moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T,
     CHECK_ARG(x && y && x != y && aligned(x, 16) && aligned(y, 2));
     cudaStream_t s = (cudaStream_t)stream;
     timing_begin(s);
+    if (T >= kLinearMatrixRows) {
+        LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)((char*)workspace + kAlign), s));
+        LAUNCH(kGroupedFwd, launch_grouped(kGmmFwd, 0, linear_gmm(W, x, T, y, workspace), s));
+        return MOE_OK;
+    }
     LAUNCH(kAffineLinear, launch_affine_linear(*W, x, T, y, s));
     return MOE_OK;
 }

@@ -113,12 +113,25 @@ def test_swiglu_grad_refuses_its_own():
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
-    """The binding takes tensors of the current device only (a stand-in tensor: no GPU is needed)."""
+    """The binding takes contiguous tensors of the current device only (stand-in tensors: no GPU is needed)."""
     torch = pytest.importorskip("torch")
 
     class Tensor:
-        is_cuda, device = True, torch.device("cuda", 1)
+        def __init__(self, device, contiguous=True):
+            self.device, self.contiguous = device, contiguous
+
+        def get_device(self):
+            return self.device
+
+        def is_contiguous(self):
+            return self.contiguous
+
+        def data_ptr(self):
+            return A
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    with pytest.raises(ValueError, match="cuda:1"):
-        moe_swiglu(0, Tensor(), None, None, 0, 4, 16, D, stream=0)
+    for bad, why in ((Tensor(1), "cuda:1"), (Tensor(-1), "CUDA"), (Tensor(0, False), "contiguous")):
+        with pytest.raises(ValueError, match=why):
+            moe_swiglu(0, bad, None, None, 0, 4, 16, D, stream=0)
+        with pytest.raises(ValueError, match=why):
+            moe_swiglu(0, Tensor(0), bad, None, 0, 4, 16, D, stream=0)
