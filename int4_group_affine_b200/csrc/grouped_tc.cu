@@ -31,6 +31,9 @@
 // the other (a fixed order).
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
+#include <string.h>
+
+#include <algorithm>
 
 #include "grouped.cuh"
 #include "tc.cuh"
@@ -38,26 +41,32 @@
 namespace moeq {
 namespace {
 
-constexpr int kLanes = 128;              // output tile: matrix rows
+constexpr int kLanes = 128;              // matrix rows of a block's part of a tile
 constexpr int kCols = 256;               // and at most this many columns
 constexpr int kStep = 64;                // terms per stage
-constexpr int kStages = 4;
 constexpr int kABytes = kLanes * 128;    // 64 16-bit terms of every lane
-constexpr int kBBytes = kCols * 128;
-constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBox = 64 * 128;           // an MN-major box: 64 terms of 64 outputs
 constexpr int kEpi = 8;                  // result warps
 constexpr int kThreads = (2 + kEpi) * 32;
 constexpr int kOutBytes = 32 * 128;      // dw: a warp's staging box
 constexpr int kPart = 512;               // fp32 dw: terms per part
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpi * kOutBytes;
-static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
+
+// Shared memory by direction and by the blocks that share a tile (kCta = 2: a cluster's pair, each loading its 128
+// rows and half of the columns).
+template <int kDir, int kCta>
+struct Ring {
+    static constexpr int outs = kDir == kGmmDw ? 2 : 0;  // a warp's staging boxes
+    static constexpr int stages = kDir == kGmmDw ? (kCta == 2 ? 5 : 3) : (kCta == 2 ? 6 : 4);
+    static constexpr int bytes = kABytes + kCols / kCta * 128;
+    static constexpr size_t smem = 1024 + stages * bytes + outs * kEpi * kOutBytes;
+    static_assert(smem + 1024 <= 227 * 1024, "shared memory");
+};
 
 struct TcGmm {
     CUtensorMap tma;     // the lanes' operand
-    CUtensorMap tmb;     // the columns' operand, in boxes of 128 rows (forward, dx) or 64 x 64 (dw)
-    CUtensorMap tmb16;   // forward, dx: the same in boxes of 16 rows
+    CUtensorMap tmb[4];  // the columns' operand: forward, dx in boxes of 16, 32, 64 and 128 rows; dw [0]
     CUtensorMap tmo;     // dw: the output, in boxes of 32 rows x 128 bytes
+    int wide_a, wide_b;  // an MN-major operand whose whole tile is one box (see encode_mn)
     GmmArgs a;
 };
 
@@ -67,13 +76,14 @@ struct Tile {
     int lane0;     // first output row of the tile
     int col0;      // first column: row of x / dy (forward, dx), input k (dw)
     int cols;      // columns that count
-    int width;     // columns multiplied: cols rounded up to 16
+    int width;     // columns multiplied: cols rounded up
     int terms;     // length of the sum
     int row0;      // dw: first row of the group
 };
 
-template <int kDir>
+template <int kDir, int kCta>
 struct Schedule {
+    static constexpr int kTileLanes = kLanes * kCta;
     GmmWalk walk;
     int g_dw = -1;
     GmmRows rows_dw;
@@ -81,43 +91,164 @@ struct Schedule {
     __device__ __forceinline__ Tile at(const GmmArgs& a, int64_t tile, int lane) {
         Tile t;
         if (kDir == kGmmDw) {
-            const int nt = (a.N + kLanes - 1) / kLanes, kt = (a.K + kCols - 1) / kCols;
+            const int nt = (a.N + kTileLanes - 1) / kTileLanes, kt = (a.K + kCols - 1) / kCols;
             const int64_t per = (int64_t)nt * kt;
             t.g = tile < per * a.G ? (int)(tile / per) : -1;
             if (t.g < 0) return t;
             if (t.g != g_dw) rows_dw = gmm_rows_of(a, g_dw = t.g, lane);
             const int rem = (int)(tile % per);
-            t.lane0 = rem / kt * kLanes;
+            t.lane0 = rem / kt * kTileLanes;
             t.col0 = rem % kt * kCols;
             t.cols = min(kCols, a.K - t.col0);
             t.terms = rows_dw.end - rows_dw.begin;
             t.row0 = rows_dw.begin;
+            t.width = kCta == 2 ? (t.cols + 127) & ~127 : (t.cols + 15) & ~15;  // (a pair's halves: whole boxes)
         } else {
-            const int J = kDir == kGmmFwd ? a.N : a.K, across = (J + kLanes - 1) / kLanes;
+            const int J = kDir == kGmmFwd ? a.N : a.K, across = (J + kTileLanes - 1) / kTileLanes;
             GmmRows r;
             int64_t within;
             t.g = walk.find(a, lane, tile, kCols, across, &r, &within);
             if (t.g < 0) return t;
             const int count = r.end - r.begin, parts = (count + kCols - 1) / kCols;
-            const int w = ((count + parts - 1) / parts + 15) & ~15;
+            constexpr int kUp = 16 * kCta;  // what the instruction's width is a multiple of
+            const int w = ((count + parts - 1) / parts + kUp - 1) & ~(kUp - 1);
             const int p = (int)(within / across);
-            t.lane0 = (int)(within % across) * kLanes;
+            t.lane0 = (int)(within % across) * kTileLanes;
             t.col0 = r.begin + p * w;
             t.cols = min(w, count - p * w);
             t.terms = kDir == kGmmFwd ? a.K : a.N;
+            t.width = (t.cols + kUp - 1) & ~(kUp - 1);
         }
-        t.width = (t.cols + 15) & ~15;
         return t;
     }
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint64_t* bar) {
+// The pipeline's two warps run their loops together and one elected lane issues (`one`): the loops' values stay
+// uniform, which the tensor core's and TMA's instructions take without a detour.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// TMA loads into this block's shared memory; a pair's loads may signal a barrier of either block (`bar`: a
+// shared::cluster address).
+#define MOEQ_TMA_LOAD(dims, coords, ...)                                                                            \
+    if (kCta == 2)                                                                                                  \
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\t@q cp.async.bulk.tensor." dims               \
+                     ".shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, " coords    \
+                     "], [%2];\n\t}" ::"r"(dst),                                                                    \
+                     "l"(map), "r"(bar), "r"(one), __VA_ARGS__                                                      \
+                     : "memory");                                                                                   \
+    else                                                                                                            \
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\t@q cp.async.bulk.tensor." dims               \
+                     ".shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, " coords                 \
+                     "], [%2];\n\t}" ::"r"(dst),                                                                    \
+                     "l"(map), "r"(bar), "r"(one), __VA_ARGS__                                                      \
+                     : "memory")
+template <int kCta>
+__device__ __forceinline__ void load_2d(uint32_t one, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+    MOEQ_TMA_LOAD("2d", "{%4, %5}", "r"(x), "r"(y));
+}
+template <int kCta>
+__device__ __forceinline__ void load_3d(uint32_t one, uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+    MOEQ_TMA_LOAD("3d", "{%4, %5, %6}", "r"(x), "r"(y), "r"(z));
+}
+template <int kCta>
+__device__ __forceinline__ void load_4d(uint32_t one, uint32_t dst, const void* map, int x, int y, int z, int w,
+                                        uint32_t bar) {
+    MOEQ_TMA_LOAD("4d", "{%4, %5, %6, %7}", "r"(x), "r"(y), "r"(z), "r"(w));
+}
+#undef MOEQ_TMA_LOAD
+__device__ __forceinline__ void expect_tx(uint32_t one, uint32_t bar, uint32_t bytes) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(one)
         : "memory");
 }
+
+// ------------------------------------------------------------------ pairs of blocks
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The address, in the cluster's shared memory, of rank 0's copy of a variable.
+__device__ __forceinline__ uint32_t in_rank0(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(0));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// tc::mbar_try_wait that also acquires what the cluster's other block released with its arrival.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+template <int kCta>
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {  // a warp of every block of the tile
+    if (kCta == 1) {
+        tc::tmem_alloc(dst, cols);
+        tc::tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(dst)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int kCta>
+__device__ __forceinline__ void tmem_free(uint32_t t, uint32_t cols) {
+    if (kCta == 1) tc::tmem_dealloc(t, cols);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
+}
+// D (+)= A B^T.
+template <int kCta>
+__device__ __forceinline__ void mma(uint32_t one, uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add) {
+    if (kCta == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(add), "r"(one)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(add), "r"(one)
+            : "memory");
+}
+// Arrive on `bar` (of both blocks of a pair) once this thread's MMAs so far are done.
+template <int kCta>
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+    if (kCta == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+            "r"(one)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+            "%2;\n\t}" ::"r"(bar),
+            "r"(one), "h"((uint16_t)3)
+            : "memory");
+}
+
 __device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
                  "r"(src), "r"(x), "r"(y), "r"(z)
@@ -130,7 +261,7 @@ __device__ __forceinline__ void tma_add_3d(const void* map, uint32_t src, int x,
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 32 lanes x 32 consecutive 32-bit columns.
@@ -158,11 +289,11 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
     return d;
 }
 
-template <int kDir>
+template <int kDir, int kCta>
 __device__ __forceinline__ uint32_t idesc_of(int f16, int width) {
     const uint32_t t = f16 ? 0u : 1u;
     return (1u << 4) | (t << 7) | (t << 10) | (kDir != kGmmFwd ? 1u << 15 : 0u) | (kDir == kGmmDw ? 1u << 16 : 0u) |
-           ((uint32_t)(width >> 3) << 17) | ((uint32_t)(kLanes >> 4) << 24);
+           ((uint32_t)(width >> 3) << 17) | ((uint32_t)(kLanes * kCta >> 4) << 24);
 }
 
 template <int kF16>
@@ -178,13 +309,44 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return (uint32_t)to16<kF16>(lo) | ((uint32_t)to16<kF16>(hi) << 16);
 }
 
+// As tc::mbar_wait_ok, for after a first try: out of the loops' code, with the device's clock (slow to read) and the
+// flag looked at once in 256 tries.  (A lone warp issues an instruction in 5 to 20 cycles and a stage's products take
+// 512 at most: with the waits in line and the values in one thread's registers the loops took 1,070.)
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* ok, uint64_t limit) {
+    uint64_t t0 = 0;
+    for (;;) {
+        for (int i = 0; i < 256; ++i)
+            if (tc::mbar_try_wait(bar, parity)) return true;
+        const uint64_t t = tc::globaltimer_ns();
+        if (*ok == 0) return false;
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit) break;
+    }
+    raise_status(status, MOE_ERR_TIMEOUT);
+    *ok = 0;
+    return false;
+}
 // A whole warp's wait: the same answer in every lane, so that a wait that gives up never splits the warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const GmmArgs& a, volatile int* ok) {
-    return __all_sync(0xffffffffu, tc::mbar_wait_ok(bar, parity, a.status, ok, a.wait_ns));
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_more(bar, parity, a.status, ok, a.wait_ns));
 }
 
-template <int kDir, int kF16>
+// A place in the ring of stages, and the parity its barriers complete with next.
+template <int kStages>
+struct Place {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == kStages) st = 0, phase ^= 1;
+    }
+};
+
+template <int kDir, int kF16, int kCta>
 __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_constant__ TcGmm p) {
+    constexpr int kStages = Ring<kDir, kCta>::stages, kStageBytes = Ring<kDir, kCta>::bytes;
+    // dw: a pair's second block clears its own operands behind the group's last row, so its loads report to its own
+    // barrier and its MMA warp passes the stage on; otherwise they report to the first block's barrier directly
+    constexpr bool kRelay = kCta == 2 && kDir == kGmmDw;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     unsigned char* s_out = sm + kStages * kStageBytes;
@@ -195,145 +357,179 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     __shared__ volatile int s_ok;
     const GmmArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int rank = kCta == 2 ? (int)cluster_rank() : 0;
+    const int64_t tile0 = blockIdx.x / kCta, tile_step = gridDim.x / kCta;
 
-    if (warp == 1) {
-        tc::tmem_alloc(&s_tmem, 512);
-        tc::tmem_relinquish();
-    }
+    if (warp == 1) tmem_alloc<kCta>(&s_tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&bar_full[i], 1);
+            tc::mbar_init(&bar_full[i], kRelay && rank == 0 ? 2 : 1);
             tc::mbar_init(&bar_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bar_acc[i], 1);
-            tc::mbar_init(&bar_free[i], kEpi);
+            tc::mbar_init(&bar_free[i], kEpi * kCta);
         }
         tc::mbar_init(&bar_drain, 1);
         tc::mbar_init_fence();
         s_ok = 1;
         tc::tma_prefetch_desc(&p.tma);
-        tc::tma_prefetch_desc(&p.tmb);
-        tc::tma_prefetch_desc(kDir == kGmmDw ? &p.tmo : &p.tmb16);
+        tc::tma_prefetch_desc(&p.tmb[0]);
+        if (kDir == kGmmDw) tc::tma_prefetch_desc(&p.tmo);
     }
     if (blockIdx.x == 0) gmm_check_offsets(a, tid, kThreads);
     tc::tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if (kCta == 2) cluster_sync();
+    else __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
-    Schedule<kDir> sched;
+    Schedule<kDir, kCta> sched;
     const bool parts = kDir == kGmmDw && a.out_f32;  // long sums in parts
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
+        Place<kStages> at;
         uint32_t n = 0;  // stages issued
-        for (int64_t tile = blockIdx.x;; tile += gridDim.x) {
+        const uint32_t own0 = tc::smem_u32(bar_full), full0 = kCta == 2 && !kRelay ? in_rank0(own0) : own0;
+        const uint32_t one = elect_one();
+        bool ok = true;
+        for (int64_t tile = tile0; ok; tile += tile_step) {
             const Tile t = sched.at(a, tile, lane);
-            if (t.g < 0 || __any_sync(0xffffffffu, !s_ok)) break;
-            if (lane == 0) {
-                const int b128 = kDir == kGmmDw ? 0 : t.width / 128, b16 = kDir == kGmmDw ? 0 : t.width % 128 / 16;
-                const int bk = kDir == kGmmDw ? (t.cols + 63) / 64 : 0;
-                const uint32_t bytes = kABytes + b128 * 128 * 128 + b16 * 16 * 128 + bk * kBox;
-                for (int k = 0; k < t.terms; k += kStep, ++n) {
-                    const int st = n % kStages;
-                    if (n >= kStages &&
-                        !tc::mbar_wait_ok(&bar_empty[st], (n / kStages - 1) & 1, a.status, &s_ok, a.wait_ns))
-                        break;
-                    const uint32_t sa = sbase + st * kStageBytes, sb = sa + kABytes;
-                    uint64_t* full = &bar_full[st];
-                    tc::mbar_arrive_expect_tx(full, bytes);
-                    if (kDir == kGmmFwd) {
-                        tma_load_3d(sa, &p.tma, k, t.lane0, t.g, full);
-                    } else if (kDir == kGmmDx) {
-                        tma_load_3d(sa, &p.tma, t.lane0, k, t.g, full);
-                        tma_load_3d(sa + kBox, &p.tma, t.lane0 + 64, k, t.g, full);
+            if (t.g < 0) break;
+            const int lanes = t.lane0 + kLanes * rank, half = t.width / kCta, col = t.col0 + half * rank;
+            const int bk = (half + 63) / 64;  // dw: boxes of 64 columns
+            const uint32_t bytes = kABytes + (kDir == kGmmDw ? (p.wide_b ? kCols / kCta / 64 : bk) * kBox : half * 128);
+            for (int k = 0; k < t.terms; k += kStep, at.next(), ++n) {
+                ok = warp_wait(&bar_empty[at.st], at.phase ^ 1, a, &s_ok);  // (free from the start)
+                if (!ok) break;
+                const uint32_t sa = sbase + at.st * kStageBytes, sb = sa + kABytes, full = full0 + 8 * at.st;
+                if (kRelay || kCta == 1) expect_tx(one, own0 + 8 * at.st, bytes);
+                else if (rank == 0) expect_tx(one, own0 + 8 * at.st, 2 * bytes);
+                if (kDir == kGmmFwd) {
+                    load_3d<kCta>(one, sa, &p.tma, k, lanes, t.g, full);
+                } else if (kDir == kGmmDx) {
+                    if (p.wide_a) {
+                        load_4d<kCta>(one, sa, &p.tma, 0, k, lanes / 64, t.g, full);
                     } else {
-                        tc::tma_load_2d(sa, &p.tma, t.lane0, t.row0 + k, full);
-                        tc::tma_load_2d(sa + kBox, &p.tma, t.lane0 + 64, t.row0 + k, full);
+                        load_3d<kCta>(one, sa, &p.tma, lanes, k, t.g, full);
+                        load_3d<kCta>(one, sa + kBox, &p.tma, lanes + 64, k, t.g, full);
                     }
-                    if (kDir == kGmmDw) {
-                        for (int i = 0; i < bk; ++i)
-                            tc::tma_load_2d(sb + i * kBox, &p.tmb, t.col0 + 64 * i, t.row0 + k, full);
+                } else if (p.wide_a) {
+                    load_3d<kCta>(one, sa, &p.tma, 0, t.row0 + k, lanes / 64, full);
+                } else {
+                    load_2d<kCta>(one, sa, &p.tma, lanes, t.row0 + k, full);
+                    load_2d<kCta>(one, sa + kBox, &p.tma, lanes + 64, t.row0 + k, full);
+                }
+                if (kDir == kGmmDw) {
+                    if (p.wide_b) {
+                        load_3d<kCta>(one, sb, &p.tmb[0], 0, t.row0 + k, col / 64, full);
                     } else {
-                        for (int i = 0; i < b128; ++i)
-                            tc::tma_load_2d(sb + i * 128 * 128, &p.tmb, k, t.col0 + 128 * i, full);
-                        for (int i = 0; i < b16; ++i)
-                            tc::tma_load_2d(sb + b128 * 128 * 128 + i * 16 * 128, &p.tmb16, k,
-                                            t.col0 + 128 * b128 + 16 * i, full);
+                        for (int i = 0; i < bk; ++i)
+                            load_2d<kCta>(one, sb + i * kBox, &p.tmb[0], col + 64 * i, t.row0 + k, full);
+                    }
+                } else {  // the width in boxes of falling powers of two
+                    if (half >= 128) load_2d<kCta>(one, sb, &p.tmb[3], k, col, full);
+                    if (kCta == 1 && half == 256) {
+                        load_2d<kCta>(one, sb + 128 * 128, &p.tmb[3], k, col + 128, full);
+                    } else if (half % 128) {
+                        int row = half & 128;
+#pragma unroll
+                        for (int i = 2; i >= 0; --i)
+                            if (half & (16 << i)) {
+                                load_2d<kCta>(one, sb + row * 128, &p.tmb[i], k, col + row, full);
+                                row += 16 << i;
+                            }
                     }
                 }
             }
-            __syncwarp();
         }
-        if (lane == 0 && !s_ok)  // given up: wait for the copies still in flight before the block ends
+        if (lane == 0 && !s_ok && (kRelay || rank == 0))
+            // given up: wait for the copies still in flight before the block ends (a pair's second block, whose
+            // copies report to the first, ends with it)
             for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
                 tc::mbar_wait(&bar_full[i % kStages], (i / kStages) & 1, a.status, a.wait_ns);
-    } else if (warp == 1) {
+    } else if (warp == 1 && (rank == 0 || kRelay)) {
         // ------------------------------------------------------------ products
-        uint32_t n = 0, acc = 0;
+        // descriptors of stage 0; a stage, and 16 terms, are so many 16-byte units further
+        constexpr uint32_t kAdvA = kDir == kGmmFwd ? 32 >> 4 : 2048 >> 4, kAdvB = kDir == kGmmDw ? 2048 >> 4 : 32 >> 4;
+        const uint64_t ad0 = kDir == kGmmFwd ? tc::sdesc_k_sw128(sbase) : sdesc_mn_sw128(sbase);
+        const uint64_t bd0 = kDir == kGmmDw ? sdesc_mn_sw128(sbase + kABytes) : tc::sdesc_k_sw128(sbase + kABytes);
+        const uint32_t empty0 = tc::smem_u32(bar_empty), acc0 = tc::smem_u32(bar_acc);
+        const uint32_t full_rank0 = kRelay ? in_rank0(tc::smem_u32(bar_full)) : 0;
+        const uint32_t one = elect_one();
+        Place<kStages> at;
+        uint32_t acc = 0;
         bool ok = true;
-        for (int64_t tile = blockIdx.x; ok; tile += gridDim.x) {
+        for (int64_t tile = tile0; ok; tile += tile_step) {
             const Tile t = sched.at(a, tile, lane);
             if (t.g < 0) break;
-            const uint32_t idesc = idesc_of<kDir>(kF16, t.width);
+            const uint32_t idesc = idesc_of<kDir, kCta>(kF16, t.width);
             for (int p0 = 0; ok && p0 < t.terms; ++acc) {
                 const int p1 = parts ? min(t.terms, p0 + kPart) : t.terms;
                 const uint32_t d = tmem + (acc & 1) * kCols;
-                if (acc >= 2) ok = warp_wait(&bar_free[acc & 1], (acc / 2 - 1) & 1, a, &s_ok);
+                if (rank == 0) ok = warp_wait(&bar_free[acc & 1], (acc / 2 & 1) ^ 1, a, &s_ok);
+                if (!ok) break;
                 tc::tc_fence_after();
-                for (int k = p0; ok && k < p1; k += kStep, ++n) {
-                    const int st = n % kStages;
-                    ok = warp_wait(&bar_full[st], (n / kStages) & 1, a, &s_ok);
+                for (int k = p0; k < p1; k += kStep, at.next()) {
+                    ok = warp_wait(&bar_full[at.st], at.phase, a, &s_ok);
                     if (!ok) break;
-                    const uint32_t sa = sbase + st * kStageBytes, sb = sa + kABytes;
-                    const int left = min(kStep, t.terms - k), m16 = (left + 15) / 16;
-                    if (kDir == kGmmDw && left % 16) {  // the rows behind the group's last, up to the next 16
-                        const int clear = (m16 * 16 - left) * 8, bk = (t.cols + 63) / 64;
-                        unsigned char* base = sm + st * kStageBytes + left * 128;
+                    const int left = t.terms - k;
+                    if (kDir == kGmmDw && left < kStep && left % 16) {  // the rows behind the group's last
+                        const int clear = ((left + 15 & ~15) - left) * 8, bk = (t.width / kCta + 63) / 64;
+                        unsigned char* base = sm + at.st * kStageBytes + left * 128;
                         for (int b = 0; b < 2 + bk; ++b)
                             for (int i = lane; i < clear; i += 32)
                                 *reinterpret_cast<uint4*>(base + b * kBox + i * 16) = make_uint4(0, 0, 0, 0);
                         tc::fence_async_smem();
                         __syncwarp();
                     }
-                    if (lane == 0) {
-                        tc::tc_fence_after();
-                        for (int s = 0; s < m16; ++s) {
-                            const uint64_t ad = kDir == kGmmFwd ? tc::sdesc_k_sw128(sa + 32 * s)
-                                                                : sdesc_mn_sw128(sa + 2048 * s);
-                            const uint64_t bd = kDir == kGmmDw ? sdesc_mn_sw128(sb + 2048 * s)
-                                                               : tc::sdesc_k_sw128(sb + 32 * s);
-                            tc::mma_bf16(d, ad, bd, idesc, k > p0 || s > 0);
-                        }
-                        tc::mma_commit(&bar_empty[st]);
+                    if (rank == 1) {  // (kRelay)
+                        if (one) arrive_cluster(full_rank0 + 8 * at.st);
+                        __syncwarp();
+                        continue;
                     }
-                    __syncwarp();
+                    if (kRelay) try_wait_cluster(&bar_full[at.st], at.phase);  // (complete: an acquire)
+                    tc::tc_fence_after();
+                    const uint64_t ad = ad0 + at.st * (kStageBytes >> 4), bd = bd0 + at.st * (kStageBytes >> 4);
+                    if (left >= kStep) {
+#pragma unroll
+                        for (int s = 0; s < kStep / 16; ++s)
+                            mma<kCta>(one, d, ad + s * kAdvA, bd + s * kAdvB, idesc, s > 0 || k > p0);
+                    } else {
+                        for (int s = 0; 16 * s < left; ++s)
+                            mma<kCta>(one, d, ad + s * kAdvA, bd + s * kAdvB, idesc, s > 0 || k > p0);
+                    }
+                    commit<kCta>(one, empty0 + 8 * at.st);
                 }
-                if (ok && lane == 0) tc::mma_commit(&bar_acc[acc & 1]);
-                __syncwarp();
+                if (ok && rank == 0) commit<kCta>(one, acc0 + 8 * (acc & 1));
                 p0 = p1;
             }
         }
-        if (!ok && lane == 0) {  // given up: the products still in flight end before their memory is freed
-            tc::mma_commit(&bar_drain);
+        if (!ok && one && rank == 0) {  // given up: the products still in flight end before their memory is freed
+            commit<kCta>(1, tc::smem_u32(&bar_drain));
             tc::mbar_wait(&bar_drain, 0, a.status, a.wait_ns);
         }
-    } else {
+    } else if (warp > 1) {
         // ------------------------------------------------------------ results
         const int q = warp % 4, half = (warp - 2) / 4;  // lanes [32 q, 32 q + 32), every other piece of columns
         uint32_t acc = 0;
         bool ok = true;
-        const uint32_t so = tc::smem_u32(s_out + (warp - 2) * kOutBytes);
-        unsigned char* sg = s_out + (warp - 2) * kOutBytes;
-        for (int64_t tile = blockIdx.x; ok; tile += gridDim.x) {
+        auto release = [&](uint64_t* bar) {  // an accumulator may be overwritten, as far as this warp goes
+            if (kCta == 2) arrive_cluster(in_rank0(tc::smem_u32(bar)));
+            else tc::mbar_arrive(bar);
+        };
+        unsigned char* boxes = s_out + (warp - 2) * 2 * kOutBytes;  // dw: two staging boxes, used in turn
+        int box = 0;
+        for (int64_t tile = tile0; ok; tile += tile_step) {
             const Tile t = sched.at(a, tile, lane);
             if (t.g < 0) break;
             if (kDir != kGmmDw) {
                 ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const int J = kDir == kGmmFwd ? a.N : a.K, f = t.lane0 + 32 * q + lane;
+                const int J = kDir == kGmmFwd ? a.N : a.K, f = t.lane0 + kLanes * rank + 32 * q + lane;
                 uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)t.col0 * J + f;
                 for (int c = 32 * half; c < t.cols; c += 64) {
                     uint32_t v[32];
@@ -349,12 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar_free[acc & 1]);
+                if (lane == 0) release(&bar_free[acc & 1]);
                 ++acc;
                 continue;
             }
             // dw: pieces of 128 bytes of every lane's row (32 fp32 or 64 16-bit columns)
-            const int n = t.lane0 + 32 * q + lane;
+            const int n0 = t.lane0 + kLanes * rank + 32 * q, n = n0 + lane;
             const int per = a.out_f32 ? 32 : 64;
             const bool empty = t.terms == 0;
             if (empty && a.accumulate) continue;
@@ -401,9 +597,12 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                                 w[16 * h + i] = pack16<kF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                         }
                     }
+                    unsigned char* sg = boxes + box * kOutBytes;
+                    const uint32_t so = tc::smem_u32(sg);
+                    box ^= 1;
                     if (lane == 0) {  // the staging box is free, and earlier parts are in place
                         if (p0 > 0) bulk_wait();
-                        else bulk_wait_read();
+                        else bulk_wait_read1();
                     }
                     __syncwarp();
 #pragma unroll
@@ -412,24 +611,26 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                     tc::fence_async_smem();
                     __syncwarp();
-                    if (lane == 0 && t.lane0 + 32 * q < a.N) {
-                        if (add && a.out_f32) tma_add_3d(&p.tmo, so, t.col0 + c, t.lane0 + 32 * q, t.g);
-                        else tma_store_3d(&p.tmo, so, t.col0 + c, t.lane0 + 32 * q, t.g);
+                    if (lane == 0 && n0 < a.N) {
+                        if (add && a.out_f32) tma_add_3d(&p.tmo, so, t.col0 + c, n0, t.g);
+                        else tma_store_3d(&p.tmo, so, t.col0 + c, n0, t.g);
                         bulk_commit();
                     }
                 }
                 if (empty) break;
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar_free[buf]);
+                if (lane == 0) release(&bar_free[buf]);
                 ++acc;
                 p0 = parts ? p0 + kPart : t.terms;
             }
         }
         if (kDir == kGmmDw && lane == 0) bulk_wait();  // the last boxes are read (and written) before the block ends
     }
-    __syncthreads();
-    if (warp == 1) tc::tmem_dealloc(tmem, 512);
+    __syncwarp();
+    if (kCta == 2) cluster_sync();  // (neither block ends while the other still reaches into it)
+    else __syncthreads();
+    if (warp == 1) tmem_free<kCta>(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -457,17 +658,47 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kDir, int kF16>
-cudaError_t launch_dir(const TcGmm& p, int64_t tiles, cudaStream_t s) {
+// An MN-major operand [outer][terms][cols] as [outer][cols / 64][terms][64]: a box of 64 terms and `blocks` column
+// blocks lands as that many 64 x 64 boxes side by side, one request instead of `blocks`.  Needs whole blocks (else a
+// row's last block would run into the next row): cols % 64 == 0.
+bool encode_mn(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t cols, int64_t terms, int64_t outer,
+               int blocks) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)terms, (cuuint64_t)(cols / 64), (cuuint64_t)(outer ? outer : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)cols * 2, 128, (cuuint64_t)cols * terms * 2};
+    const cuuint32_t box[4] = {64, 64, (cuuint32_t)blocks, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return encode_fn()(m, type, outer ? 4 : 3, const_cast<void*>(base), dims, strides, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kDir, int kF16, int kCta>
+cudaError_t launch_cta(const TcGmm& p, int64_t tiles, cudaStream_t s) {
     int dev = 0, nsm = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute((const void*)gmm_tc_kernel<kDir, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmem);
+        e = cudaFuncSetAttribute((const void*)gmm_tc_kernel<kDir, kF16, kCta>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<kDir, kCta>::smem);
     if (e != cudaSuccess) return e;
-    gmm_tc_kernel<kDir, kF16><<<(unsigned)(tiles < nsm ? tiles : nsm), kThreads, kSmem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, nsm / kCta) * kCta);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<kDir, kCta>::smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCta;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gmm_tc_kernel<kDir, kF16, kCta>, p);
+}
+
+template <int kDir, int kF16>
+cudaError_t launch_dir(const TcGmm& p, int pair, int64_t tiles, cudaStream_t s) {
+    return pair ? launch_cta<kDir, kF16, 2>(p, tiles, s) : launch_cta<kDir, kF16, 1>(p, tiles, s);
 }
 
 inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -486,27 +717,30 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s
     TcGmm p;
     p.a = a;
     const CUtensorMapDataType t = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const int64_t nt = (a.N + kLanes - 1) / kLanes;
-    int64_t tiles;
+    const int64_t J = dir == kGmmDx ? a.K : a.N;  // the lanes' side
+    const int pair = J > kLanes, per = kLanes << pair;
+    int64_t tiles = (J + per - 1) / per;
     bool ok;
+    p.wide_a = dir == kGmmDx ? a.K % 64 == 0 : dir == kGmmDw && a.N % 64 == 0;
+    p.wide_b = dir == kGmmDw && a.K % 64 == 0;
     if (dir == kGmmDw) {
-        ok = encode(&p.tma, t, 2, a.a, a.N, a.M, 0, 64) && encode(&p.tmb, t, 2, a.b, a.K, a.M, 0, 64) &&
+        ok = (p.wide_a ? encode_mn(&p.tma, t, a.a, a.N, a.M, 0, 2) : encode(&p.tma, t, 2, a.a, a.N, a.M, 0, 64)) &&
+             (p.wide_b ? encode_mn(&p.tmb[0], t, a.b, a.K, a.M, 0, kCols / 64 >> pair) : encode(&p.tmb[0], t, 2, a.b, a.K, a.M, 0, 64)) &&
              encode(&p.tmo, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : t, a.out_f32 ? 4 : 2, a.out, a.K, a.N, a.G,
                     32);
-        p.tmb16 = p.tmb;
-        tiles = a.G * nt * ((a.K + kCols - 1) / kCols);
+        tiles *= a.G * (((int64_t)a.K + kCols - 1) / kCols);
     } else {
         const int64_t terms = dir == kGmmFwd ? a.K : a.N;
-        ok = encode(&p.tma, t, 2, a.b, a.K, a.N, a.G, dir == kGmmFwd ? kLanes : 64) &&
-             encode(&p.tmb, t, 2, a.a, terms, a.M, 0, 128) && encode(&p.tmb16, t, 2, a.a, terms, a.M, 0, 16);
-        p.tmo = p.tmb;
-        tiles = (a.M / kCols + (a.off ? (int64_t)a.G : 1)) * (dir == kGmmFwd ? nt : (a.K + kLanes - 1) / kLanes);
+        ok = p.wide_a ? encode_mn(&p.tma, t, a.b, a.K, a.N, a.G, 2)
+                      : encode(&p.tma, t, 2, a.b, a.K, a.N, a.G, dir == kGmmFwd ? kLanes : 64);
+        for (int i = 0; i < 4; ++i) ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, 16 << i);
+        tiles *= a.M / kCols + (a.off ? (int64_t)a.G : 1);
     }
     if (!ok) return cudaErrorInvalidValue;
     switch (dir) {
-        case kGmmFwd: return f16 ? launch_dir<kGmmFwd, 1>(p, tiles, s) : launch_dir<kGmmFwd, 0>(p, tiles, s);
-        case kGmmDx: return f16 ? launch_dir<kGmmDx, 1>(p, tiles, s) : launch_dir<kGmmDx, 0>(p, tiles, s);
-        default: return f16 ? launch_dir<kGmmDw, 1>(p, tiles, s) : launch_dir<kGmmDw, 0>(p, tiles, s);
+        case kGmmFwd: return f16 ? launch_dir<kGmmFwd, 1>(p, pair, tiles, s) : launch_dir<kGmmFwd, 0>(p, pair, tiles, s);
+        case kGmmDx: return f16 ? launch_dir<kGmmDx, 1>(p, pair, tiles, s) : launch_dir<kGmmDx, 0>(p, pair, tiles, s);
+        default: return f16 ? launch_dir<kGmmDw, 1>(p, pair, tiles, s) : launch_dir<kGmmDw, 0>(p, pair, tiles, s);
     }
 }
 
