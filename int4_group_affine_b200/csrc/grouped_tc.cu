@@ -56,7 +56,7 @@ constexpr int kPart = 512;               // fp32 dw: terms per part
 template <int kDir, int kCta>
 struct Ring {
     static constexpr int outs = kDir == kGmmDw ? 2 : 0;  // a warp's staging boxes
-    static constexpr int stages = kDir == kGmmDw ? (kCta == 2 ? 5 : 3) : (kCta == 2 ? 6 : 4);
+    static constexpr int stages = kDir == kGmmDw ? 3 : kCta == 2 ? 6 : 4;
     static constexpr int bytes = kABytes + kCols / kCta * 128;
     static constexpr size_t smem = 1024 + stages * bytes + outs * kEpi * kOutBytes;
     static_assert(smem + 1024 <= 227 * 1024, "shared memory");
@@ -81,43 +81,90 @@ struct Tile {
     int row0;      // dw: first row of the group
 };
 
+// n / d and n % d for small n (a quotient below 2^22), without the integer division's hundred instructions.
+struct Quot {
+    int q, r;
+};
+__device__ __forceinline__ Quot quot(int n, int d, float inv) {
+    int q = (int)((float)n * inv), r = n - q * d;
+    while (r < 0) --q, r += d;
+    while (r >= d) ++q, r -= d;
+    return Quot{q, r};
+}
+
+// The tiles of a block (or pair), one after the other.  Every warp role walks them for itself, and a tile of a small
+// group is over in 2,000 cycles: tile indices advance by additions, and a group is looked up once.
 template <int kDir, int kCta>
 struct Schedule {
     static constexpr int kTileLanes = kLanes * kCta;
+    static constexpr int kUp = 16 * kCta;  // what the instruction's width is a multiple of
     GmmWalk walk;
-    int g_dw = -1;
-    GmmRows rows_dw;
+    GmmRows rows;
+    int g = -1, across, left;              // left: tiles (forward, dx: of this group) from this one on
+    int within, step, step_g;              // dw: tile within the group, and the stride in groups and tiles
+    int parts, width;                      // forward, dx: tiles along the group's rows, and their width
+    int64_t tile;
+    float inv;
 
-    __device__ __forceinline__ Tile at(const GmmArgs& a, int64_t tile, int lane) {
+    __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane) {
+        if (kDir == kGmmDw) {
+            across = (a.K + kCols - 1) / kCols;
+            left = (a.N + kTileLanes - 1) / kTileLanes * across;  // tiles of a group
+            g = (int)(first / left);
+            within = (int)(first % left);
+            step_g = (int)(stride / left);
+            step = (int)(stride % left);
+            if (g < a.G) rows = gmm_rows_of(a, g, lane);
+        } else {
+            across = ((kDir == kGmmFwd ? a.N : a.K) + kTileLanes - 1) / kTileLanes;
+            tile = first;
+            step = (int)stride;
+            left = 0;
+        }
+        inv = 1.0f / (float)across;
+    }
+
+    // The next tile; g = -1 when there is none.
+    __device__ __forceinline__ Tile next(const GmmArgs& a, int lane) {
         Tile t;
         if (kDir == kGmmDw) {
-            const int nt = (a.N + kTileLanes - 1) / kTileLanes, kt = (a.K + kCols - 1) / kCols;
-            const int64_t per = (int64_t)nt * kt;
-            t.g = tile < per * a.G ? (int)(tile / per) : -1;
+            t.g = g < a.G ? g : -1;
             if (t.g < 0) return t;
-            if (t.g != g_dw) rows_dw = gmm_rows_of(a, g_dw = t.g, lane);
-            const int rem = (int)(tile % per);
-            t.lane0 = rem / kt * kTileLanes;
-            t.col0 = rem % kt * kCols;
+            const Quot p = quot(within, across, inv);
+            t.lane0 = p.q * kTileLanes;
+            t.col0 = p.r * kCols;
             t.cols = min(kCols, a.K - t.col0);
-            t.terms = rows_dw.end - rows_dw.begin;
-            t.row0 = rows_dw.begin;
-            t.width = kCta == 2 ? (t.cols + 127) & ~127 : (t.cols + 15) & ~15;  // (a pair's halves: whole boxes)
+            t.width = (t.cols + kUp - 1) & ~(kUp - 1);
+            t.terms = rows.end - rows.begin;
+            t.row0 = rows.begin;
+            within += step;
+            int ng = g + step_g;
+            if (within >= left) within -= left, ++ng;
+            if (ng != g && ng < a.G) rows = gmm_rows_of(a, ng, lane);
+            g = ng;
         } else {
-            const int J = kDir == kGmmFwd ? a.N : a.K, across = (J + kTileLanes - 1) / kTileLanes;
-            GmmRows r;
-            int64_t within;
-            t.g = walk.find(a, lane, tile, kCols, across, &r, &within);
-            if (t.g < 0) return t;
-            const int count = r.end - r.begin, parts = (count + kCols - 1) / kCols;
-            constexpr int kUp = 16 * kCta;  // what the instruction's width is a multiple of
-            const int w = ((count + parts - 1) / parts + kUp - 1) & ~(kUp - 1);
-            const int p = (int)(within / across);
-            t.lane0 = (int)(within % across) * kTileLanes;
-            t.col0 = r.begin + p * w;
-            t.cols = min(w, count - p * w);
+            if (left <= 0) {  // another group
+                int64_t w;
+                g = walk.find(a, lane, tile, kCols, across, &rows, &w);
+                t.g = g;
+                if (g < 0) return t;
+                const int count = rows.end - rows.begin;
+                parts = (count + kCols - 1) / kCols;
+                width = parts == 1 ? count : (count + parts - 1) / parts;
+                width = (width + kUp - 1) & ~(kUp - 1);
+                within = (int)w;
+                left = parts * across - within;
+            }
+            t.g = g;
+            const Quot p = quot(within, across, inv);
+            t.lane0 = p.r * kTileLanes;
+            t.col0 = rows.begin + p.q * width;
+            t.cols = min(width, rows.end - t.col0);
             t.terms = kDir == kGmmFwd ? a.K : a.N;
             t.width = (t.cols + kUp - 1) & ~(kUp - 1);
+            within += step;
+            left -= step;
+            tile += step;
         }
         return t;
     }
@@ -186,19 +233,6 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// tc::mbar_try_wait that also acquires what the cluster's other block released with its arrival.
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 template <int kCta>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {  // a warp of every block of the tile
     if (kCta == 1) {
@@ -344,9 +378,7 @@ struct Place {
 template <int kDir, int kF16, int kCta>
 __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_constant__ TcGmm p) {
     constexpr int kStages = Ring<kDir, kCta>::stages, kStageBytes = Ring<kDir, kCta>::bytes;
-    // dw: a pair's second block clears its own operands behind the group's last row, so its loads report to its own
-    // barrier and its MMA warp passes the stage on; otherwise they report to the first block's barrier directly
-    constexpr bool kRelay = kCta == 2 && kDir == kGmmDw;
+    static_assert(kDir != kGmmDw || kCta == 1, "dw clears operands behind the group's last row: a block's own");
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     unsigned char* s_out = sm + kStages * kStageBytes;
@@ -358,12 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     const GmmArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = kCta == 2 ? (int)cluster_rank() : 0;
-    const int64_t tile0 = blockIdx.x / kCta, tile_step = gridDim.x / kCta;
 
     if (warp == 1) tmem_alloc<kCta>(&s_tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&bar_full[i], kRelay && rank == 0 ? 2 : 1);
+            tc::mbar_init(&bar_full[i], 1);
             tc::mbar_init(&bar_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -386,27 +417,27 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
     Schedule<kDir, kCta> sched;
+    sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane);
     const bool parts = kDir == kGmmDw && a.out_f32;  // long sums in parts
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         Place<kStages> at;
         uint32_t n = 0;  // stages issued
-        const uint32_t own0 = tc::smem_u32(bar_full), full0 = kCta == 2 && !kRelay ? in_rank0(own0) : own0;
+        const uint32_t own0 = tc::smem_u32(bar_full), full0 = kCta == 2 ? in_rank0(own0) : own0;
         const uint32_t one = elect_one();
         bool ok = true;
-        for (int64_t tile = tile0; ok; tile += tile_step) {
-            const Tile t = sched.at(a, tile, lane);
+        while (ok) {
+            const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
             const int lanes = t.lane0 + kLanes * rank, half = t.width / kCta, col = t.col0 + half * rank;
             const int bk = (half + 63) / 64;  // dw: boxes of 64 columns
-            const uint32_t bytes = kABytes + (kDir == kGmmDw ? (p.wide_b ? kCols / kCta / 64 : bk) * kBox : half * 128);
+            const uint32_t bytes = kABytes + (kDir == kGmmDw ? (p.wide_b ? kCols / 64 : bk) * kBox : half * 128);
             for (int k = 0; k < t.terms; k += kStep, at.next(), ++n) {
                 ok = warp_wait(&bar_empty[at.st], at.phase ^ 1, a, &s_ok);  // (free from the start)
                 if (!ok) break;
                 const uint32_t sa = sbase + at.st * kStageBytes, sb = sa + kABytes, full = full0 + 8 * at.st;
-                if (kRelay || kCta == 1) expect_tx(one, own0 + 8 * at.st, bytes);
-                else if (rank == 0) expect_tx(one, own0 + 8 * at.st, 2 * bytes);
+                if (rank == 0) expect_tx(one, own0 + 8 * at.st, kCta * bytes);
                 if (kDir == kGmmFwd) {
                     load_3d<kCta>(one, sa, &p.tma, k, lanes, t.g, full);
                 } else if (kDir == kGmmDx) {
@@ -445,31 +476,30 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 }
             }
         }
-        if (lane == 0 && !s_ok && (kRelay || rank == 0))
+        if (lane == 0 && !s_ok && rank == 0)
             // given up: wait for the copies still in flight before the block ends (a pair's second block, whose
             // copies report to the first, ends with it)
             for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
                 tc::mbar_wait(&bar_full[i % kStages], (i / kStages) & 1, a.status, a.wait_ns);
-    } else if (warp == 1 && (rank == 0 || kRelay)) {
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ products
         // descriptors of stage 0; a stage, and 16 terms, are so many 16-byte units further
         constexpr uint32_t kAdvA = kDir == kGmmFwd ? 32 >> 4 : 2048 >> 4, kAdvB = kDir == kGmmDw ? 2048 >> 4 : 32 >> 4;
         const uint64_t ad0 = kDir == kGmmFwd ? tc::sdesc_k_sw128(sbase) : sdesc_mn_sw128(sbase);
         const uint64_t bd0 = kDir == kGmmDw ? sdesc_mn_sw128(sbase + kABytes) : tc::sdesc_k_sw128(sbase + kABytes);
         const uint32_t empty0 = tc::smem_u32(bar_empty), acc0 = tc::smem_u32(bar_acc);
-        const uint32_t full_rank0 = kRelay ? in_rank0(tc::smem_u32(bar_full)) : 0;
         const uint32_t one = elect_one();
         Place<kStages> at;
         uint32_t acc = 0;
         bool ok = true;
-        for (int64_t tile = tile0; ok; tile += tile_step) {
-            const Tile t = sched.at(a, tile, lane);
+        while (ok) {
+            const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
             const uint32_t idesc = idesc_of<kDir, kCta>(kF16, t.width);
             for (int p0 = 0; ok && p0 < t.terms; ++acc) {
                 const int p1 = parts ? min(t.terms, p0 + kPart) : t.terms;
                 const uint32_t d = tmem + (acc & 1) * kCols;
-                if (rank == 0) ok = warp_wait(&bar_free[acc & 1], (acc / 2 & 1) ^ 1, a, &s_ok);
+                ok = warp_wait(&bar_free[acc & 1], (acc / 2 & 1) ^ 1, a, &s_ok);
                 if (!ok) break;
                 tc::tc_fence_after();
                 for (int k = p0; k < p1; k += kStep, at.next()) {
@@ -477,20 +507,17 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                     if (!ok) break;
                     const int left = t.terms - k;
                     if (kDir == kGmmDw && left < kStep && left % 16) {  // the rows behind the group's last
-                        const int clear = ((left + 15 & ~15) - left) * 8, bk = (t.width / kCta + 63) / 64;
-                        unsigned char* base = sm + at.st * kStageBytes + left * 128;
-                        for (int b = 0; b < 2 + bk; ++b)
-                            for (int i = lane; i < clear; i += 32)
-                                *reinterpret_cast<uint4*>(base + b * kBox + i * 16) = make_uint4(0, 0, 0, 0);
+                        unsigned char* base = sm + at.st * kStageBytes + lane * 16;
+                        const int end = left + 15 & ~15;
+                        for (int r = left; r < end; r += 4)  // four 128-byte rows of every box at a time
+                            if (r + lane / 8 < end) {
+#pragma unroll
+                                for (int b = 0; b < kStageBytes / kBox; ++b)
+                                    *reinterpret_cast<uint4*>(base + b * kBox + r * 128) = make_uint4(0, 0, 0, 0);
+                            }
                         tc::fence_async_smem();
                         __syncwarp();
                     }
-                    if (rank == 1) {  // (kRelay)
-                        if (one) arrive_cluster(full_rank0 + 8 * at.st);
-                        __syncwarp();
-                        continue;
-                    }
-                    if (kRelay) try_wait_cluster(&bar_full[at.st], at.phase);  // (complete: an acquire)
                     tc::tc_fence_after();
                     const uint64_t ad = ad0 + at.st * (kStageBytes >> 4), bd = bd0 + at.st * (kStageBytes >> 4);
                     if (left >= kStep) {
@@ -503,11 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                     }
                     commit<kCta>(one, empty0 + 8 * at.st);
                 }
-                if (ok && rank == 0) commit<kCta>(one, acc0 + 8 * (acc & 1));
+                if (ok) commit<kCta>(one, acc0 + 8 * (acc & 1));
                 p0 = p1;
             }
         }
-        if (!ok && one && rank == 0) {  // given up: the products still in flight end before their memory is freed
+        if (!ok && one) {  // given up: the products still in flight end before their memory is freed
             commit<kCta>(1, tc::smem_u32(&bar_drain));
             tc::mbar_wait(&bar_drain, 0, a.status, a.wait_ns);
         }
@@ -522,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         };
         unsigned char* boxes = s_out + (warp - 2) * 2 * kOutBytes;  // dw: two staging boxes, used in turn
         int box = 0;
-        for (int64_t tile = tile0; ok; tile += tile_step) {
-            const Tile t = sched.at(a, tile, lane);
+        while (ok) {
+            const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
             if (kDir != kGmmDw) {
                 ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
@@ -698,7 +725,9 @@ cudaError_t launch_cta(const TcGmm& p, int64_t tiles, cudaStream_t s) {
 
 template <int kDir, int kF16>
 cudaError_t launch_dir(const TcGmm& p, int pair, int64_t tiles, cudaStream_t s) {
-    return pair ? launch_cta<kDir, kF16, 2>(p, tiles, s) : launch_cta<kDir, kF16, 1>(p, tiles, s);
+    if constexpr (kDir != kGmmDw)
+        if (pair) return launch_cta<kDir, kF16, 2>(p, tiles, s);
+    return launch_cta<kDir, kF16, 1>(p, tiles, s);
 }
 
 inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -718,14 +747,14 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s
     p.a = a;
     const CUtensorMapDataType t = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t J = dir == kGmmDx ? a.K : a.N;  // the lanes' side
-    const int pair = J > kLanes, per = kLanes << pair;
+    const int pair = dir != kGmmDw && J > kLanes, per = kLanes << pair;
     int64_t tiles = (J + per - 1) / per;
     bool ok;
     p.wide_a = dir == kGmmDx ? a.K % 64 == 0 : dir == kGmmDw && a.N % 64 == 0;
     p.wide_b = dir == kGmmDw && a.K % 64 == 0;
     if (dir == kGmmDw) {
         ok = (p.wide_a ? encode_mn(&p.tma, t, a.a, a.N, a.M, 0, 2) : encode(&p.tma, t, 2, a.a, a.N, a.M, 0, 64)) &&
-             (p.wide_b ? encode_mn(&p.tmb[0], t, a.b, a.K, a.M, 0, kCols / 64 >> pair) : encode(&p.tmb[0], t, 2, a.b, a.K, a.M, 0, 64)) &&
+             (p.wide_b ? encode_mn(&p.tmb[0], t, a.b, a.K, a.M, 0, kCols / 64) : encode(&p.tmb[0], t, 2, a.b, a.K, a.M, 0, 64)) &&
              encode(&p.tmo, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : t, a.out_f32 ? 4 : 2, a.out, a.K, a.N, a.G,
                     32);
         tiles *= a.G * (((int64_t)a.K + kCols - 1) / kCols);
