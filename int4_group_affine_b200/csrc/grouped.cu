@@ -68,7 +68,7 @@ template <int kDir, int kF16>
 __global__ void __launch_bounds__(kThreads) gmm_any_kernel(const GmmArgs a) {
     __shared__ __align__(16) uint16_t sA[kT][kPitch], sB[kT][kPitch];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g8 = lane / 4, c4 = lane % 4;
-    if (blockIdx.x == 0) gmm_check_offsets(a, tid, kThreads);
+    if (blockIdx.x == 0) (void)gmm_check_offsets(a, tid, kThreads);
 
     // the tile: group, output rows [i0, I) and columns [j0, J), terms [0, S)
     const int J = kDir == kGmmFwd ? a.N : a.K;

@@ -106,14 +106,17 @@ struct GmmWalk {
     }
 };
 
-// Raises MOE_ERR_DEVICE_INDEX when the offsets are not a non-decreasing sequence within [0, M]
-// (one block's threads, any count).
-__device__ __forceinline__ void gmm_check_offsets(const GmmArgs& a, int tid, int nthreads) {
-    if (!a.off) return;
+// Whether this thread's share of the offsets (one block's threads, any count) is a non-decreasing sequence within
+// [0, M]; the first block raises MOE_ERR_DEVICE_INDEX where it is not.
+__device__ __forceinline__ bool gmm_check_offsets(const GmmArgs& a, int tid, int nthreads) {
+    if (!a.off) return true;
+    bool good = true;
     for (int g = tid; g <= a.G; g += nthreads) {
         const int v = __ldg(a.off + g);
-        if (v < 0 || v > a.M || (g > 0 && __ldg(a.off + g - 1) > v)) raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+        if (v < 0 || v > a.M || (g > 0 && __ldg(a.off + g - 1) > v)) good = false;
     }
+    if (!good && blockIdx.x == 0) raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+    return good;
 }
 
 }  // namespace moeq

@@ -99,14 +99,16 @@ struct Schedule {
     static constexpr int kTileLanes = kLanes * kCta;
     static constexpr int kUp = 16 * kCta;  // what the instruction's width is a multiple of
     GmmWalk walk;
-    GmmRows rows;
+    GmmRows rows;                          // (dw: as read, ahead of the tile)
+    bool good;
     int g = -1, across, left;              // left: tiles (forward, dx: of this group) from this one on
     int within, step, step_g;              // dw: tile within the group, and the stride in groups and tiles
     int parts, width;                      // forward, dx: tiles along the group's rows, and their width
     int64_t tile;
     float inv;
 
-    __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane) {
+    __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane, bool good_) {
+        good = good_;
         if (kDir == kGmmDw) {
             across = (a.K + kCols - 1) / kCols;
             left = (a.N + kTileLanes - 1) / kTileLanes * across;  // tiles of a group
@@ -114,7 +116,7 @@ struct Schedule {
             within = (int)(first % left);
             step_g = (int)(stride / left);
             step = (int)(stride % left);
-            if (g < a.G) rows = gmm_rows_of(a, g, lane);
+            fetch(a, lane);
         } else {
             across = ((kDir == kGmmFwd ? a.N : a.K) + kTileLanes - 1) / kTileLanes;
             tile = first;
@@ -122,6 +124,13 @@ struct Schedule {
             left = 0;
         }
         inv = 1.0f / (float)across;
+    }
+
+    // dw: the rows of group g, on their way while the tile before them is worked on.
+    __device__ __forceinline__ void fetch(const GmmArgs& a, int lane) {
+        if (g >= a.G) return;
+        if (!good) rows = gmm_rows_of(a, g, lane);
+        else rows = a.off ? GmmRows{__ldg(a.off + g), __ldg(a.off + g + 1)} : GmmRows{0, a.M};
     }
 
     // The next tile; g = -1 when there is none.
@@ -140,8 +149,10 @@ struct Schedule {
             within += step;
             int ng = g + step_g;
             if (within >= left) within -= left, ++ng;
-            if (ng != g && ng < a.G) rows = gmm_rows_of(a, ng, lane);
-            g = ng;
+            if (ng != g) {
+                g = ng;
+                fetch(a, lane);
+            }
         } else {
             if (left <= 0) {  // another group
                 int64_t w;
@@ -339,8 +350,14 @@ __device__ __forceinline__ float from16(uint16_t v) {
     return kF16 ? __half2float(__ushort_as_half(v)) : bf16f(v);
 }
 template <int kF16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-    return (uint32_t)to16<kF16>(lo) | ((uint32_t)to16<kF16>(hi) << 16);
+__device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi) {  // (fp32 bit patterns)
+    const float2 v = make_float2(__uint_as_float(lo), __uint_as_float(hi));
+    if (kF16) {
+        const __half2 h = __float22half2_rn(v);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 b = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // As tc::mbar_wait_ok, for after a first try: out of the loops' code, with the device's clock (slow to read) and the
@@ -408,16 +425,21 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         tc::tma_prefetch_desc(&p.tmb[0]);
         if (kDir == kGmmDw) tc::tma_prefetch_desc(&p.tmo);
     }
-    if (blockIdx.x == 0) gmm_check_offsets(a, tid, kThreads);
+    bool good = true;  // the offsets are in order, so a group's rows need no look at the groups before it
+    if (kDir == kGmmDw) good = gmm_check_offsets(a, tid, kThreads);
+    else if (blockIdx.x == 0) (void)gmm_check_offsets(a, tid, kThreads);
     tc::tc_fence_before();
-    __syncwarp();
-    if (kCta == 2) cluster_sync();
-    else __syncthreads();
+    if (kCta == 2) {
+        __syncwarp();
+        cluster_sync();
+    } else {
+        good = __syncthreads_and(good);
+    }
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
     Schedule<kDir, kCta> sched;
-    sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane);
+    sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane, good);
     const bool parts = kDir == kGmmDw && a.out_f32;  // long sums in parts
 
     if (warp == 0) {
@@ -549,6 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         };
         unsigned char* boxes = s_out + (warp - 2) * 2 * kOutBytes;  // dw: two staging boxes, used in turn
         int box = 0;
+        const int J = kDir == kGmmFwd ? a.N : a.K;
+        const bool pairs = J % 2 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
         while (ok) {
             const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
@@ -556,18 +580,33 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const int J = kDir == kGmmFwd ? a.N : a.K, f = t.lane0 + kLanes * rank + 32 * q + lane;
-                uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)t.col0 * J + f;
+                const int f = t.lane0 + kLanes * rank + 32 * q + lane;
+                const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + (acc & 1) * kCols;
+                uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)t.col0 * J;
                 for (int c = 32 * half; c < t.cols; c += 64) {
                     uint32_t v[32];
-                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (acc & 1) * kCols + c, v);
+                    tmem_ld32(d + c, v);
                     tc::tmem_wait_ld();
                     const int live = f < J ? t.cols - c : 0;
-                    uint16_t* o = out + (int64_t)c * J;
+                    if (pairs) {
+                        // neighbouring lanes exchange, so that each stores two outputs of one row: the even lane
+                        // of the first of two rows, the odd lane of the second
+                        uint16_t* o = out + (int64_t)(c + (lane & 1)) * J + (f & ~1);
+                        const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (i < live) *o = to16<kF16>(__uint_as_float(v[i]));
-                        o += J;
+                        for (int i = 0; i < 32; i += 2) {
+                            const uint32_t mine = pack16<kF16>(v[i], v[i + 1]);
+                            const uint32_t two = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
+                            if (i + (lane & 1) < live) *reinterpret_cast<uint32_t*>(o) = two;
+                            o += 2 * J;
+                        }
+                    } else {
+                        uint16_t* o = out + (int64_t)c * J + f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (i < live) *o = to16<kF16>(__uint_as_float(v[i]));
+                            o += J;
+                        }
                     }
                 }
                 tc::tc_fence_before();
@@ -598,11 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                         tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c, w);
                         tc::tmem_wait_ld();
                     } else {
+                        uint32_t vv[2][32];
+                        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c, vv[0]);
+                        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c + 32, vv[1]);
+                        tc::tmem_wait_ld();
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            uint32_t v[32];
-                            tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c + 32 * h, v);
-                            tc::tmem_wait_ld();
+                            uint32_t(&v)[32] = vv[h];
                             if (add) {  // the earlier gradient, added in fp32 and rounded once
                                 const uint16_t* old = reinterpret_cast<const uint16_t*>(a.out) +
                                                       ((int64_t)t.g * a.N + n) * a.K + t.col0 + c + 32 * h;
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                             }
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                w[16 * h + i] = pack16<kF16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                                w[16 * h + i] = pack16<kF16>(v[2 * i], v[2 * i + 1]);
                         }
                     }
                     unsigned char* sg = boxes + box * kOutBytes;
