@@ -928,6 +928,9 @@ moe_status linear_check(const moe_qtensor* W) {
     return MOE_OK;
 }
 
+// Whether a forward of T rows multiplies the matrix in bf16 (else the codes).
+bool linear_matrix(const moe_qtensor* W, int T) { return T >= kLinearMatrixRows || !affine_codes_supported(*W); }
+
 // status word, then the matrix as bf16 where the call multiplies that
 size_t linear_bytes(const moe_qtensor* W, bool matrix) {
     return kAlign + (matrix ? align_up((size_t)W->out * W->in * 2) : 0);
@@ -952,7 +955,7 @@ GmmArgs linear_gmm(const moe_qtensor* W, const uint16_t* rows, int T, uint16_t* 
 
 size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T) {
     if (T < 0 || linear_check(W) != MOE_OK) return 0;
-    return linear_bytes(W, T >= kLinearMatrixRows);
+    return linear_bytes(W, linear_matrix(W, T));
 }
 
 moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y, void* workspace,
@@ -966,7 +969,7 @@ moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T,
     CHECK_ARG(x && y && x != y && aligned(x, 16) && aligned(y, 2));
     cudaStream_t s = (cudaStream_t)stream;
     timing_begin(s);
-    if (T >= kLinearMatrixRows) {
+    if (linear_matrix(W, T)) {
         LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)((char*)workspace + kAlign), s));
         LAUNCH(kGroupedFwd, launch_grouped(kGmmFwd, 0, linear_gmm(W, x, T, y, workspace), s));
         return MOE_OK;

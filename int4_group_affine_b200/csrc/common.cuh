@@ -267,6 +267,7 @@ cudaError_t launch_ep_combine(const uint16_t* ret, const int32_t* pos, const flo
                               const float* sg, int T, int K, int H, uint16_t* y, cudaStream_t s);
 
 // Rows times an affine-packed matrix (csrc/linear.cu): y bf16 [T][out]; the matrix as bf16 [out][in].
+bool affine_codes_supported(const moe_qtensor& W);
 cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T, uint16_t* y, cudaStream_t s);
 cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s);
 

@@ -55,8 +55,8 @@ constexpr int kPart = 512;               // fp32 dw: terms per part
 // rows and half of the columns).
 template <int kDir, int kCta>
 struct Ring {
-    static constexpr int outs = kDir == kGmmDw ? 2 : 0;  // a warp's staging boxes
-    static constexpr int stages = kDir == kGmmDw ? 3 : kCta == 2 ? 6 : 4;
+    static constexpr int outs = kDir == kGmmDw ? 1 : 0;  // a result warp's staging boxes
+    static constexpr int stages = kCta == 2 ? 6 : 4;
     static constexpr int bytes = kABytes + kCols / kCta * 128;
     static constexpr size_t smem = 1024 + stages * bytes + outs * kEpi * kOutBytes;
     static_assert(smem + 1024 <= 227 * 1024, "shared memory");
@@ -306,7 +306,7 @@ __device__ __forceinline__ void tma_add_3d(const void* map, uint32_t src, int x,
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 32 lanes x 32 consecutive 32-bit columns.
@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             if (kCta == 2) arrive_cluster(in_rank0(tc::smem_u32(bar)));
             else tc::mbar_arrive(bar);
         };
-        unsigned char* boxes = s_out + (warp - 2) * 2 * kOutBytes;  // dw: two staging boxes, used in turn
-        int box = 0;
+        unsigned char* sg = s_out + (warp - 2) * kOutBytes;  // dw: the staging box
+        const uint32_t so = tc::smem_u32(sg);
         const int J = kDir == kGmmFwd ? a.N : a.K;
         const bool pairs = J % 2 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
         while (ok) {
@@ -665,12 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                                 w[16 * h + i] = pack16<kF16>(v[2 * i], v[2 * i + 1]);
                         }
                     }
-                    unsigned char* sg = boxes + box * kOutBytes;
-                    const uint32_t so = tc::smem_u32(sg);
-                    box ^= 1;
                     if (lane == 0) {  // the staging box is free, and earlier parts are in place
                         if (p0 > 0) bulk_wait();
-                        else bulk_wait_read1();
+                        else bulk_wait_read();
                     }
                     __syncwarp();
 #pragma unroll

@@ -30,7 +30,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRows = 16;                        // matrix rows of a tile
 constexpr int kQuad = 4;                         // units loaded together
-constexpr size_t kMaxSmem = 220 * 1024;
+constexpr size_t kMaxSmem = 226 * 1024;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -65,74 +65,75 @@ struct LinArgs {
     int vec;      // scales and biases of four units can be loaded together
 };
 
-// The words of kQuad units of the lane's two rows, and the units' scales and biases.
+// A quad's words of a tile's 16 rows in a warp's ring, in 16-byte pieces that change places by row so that the
+// fragment loads (a unit's quarters of eight rows at once) meet no two in one bank.
 template <int kBits, int kUnit>
-struct Quad {
-    static constexpr int kWords = kUnit * kBits / 128;  // words of a unit's quarter: 1, 2 or 4
-    uint32_t w[2][kQuad][kWords];
-    uint32_t s[2][kQuad / 2], b[2][kQuad / 2];  // bf16 pairs
+struct Slot {
+    static constexpr int kWords = kUnit * kBits / 128;             // words of a unit's quarter: 1, 2 or 4
+    static constexpr int kPieces = kQuad * kWords;                 // 16-byte pieces of a row: 4, 8 or 16
+    static constexpr int kCopies = kRows * kPieces / 32;           // per lane
+    static constexpr int kBytes = kRows * kPieces * 16 + 2 * kRows * kQuad * 2;  // and the scales and biases
+    static constexpr int kDepth = kWords == 4 ? 3 : 4;             // quads in the ring
+    __device__ static __forceinline__ int piece(int row, int i) {
+        return row * kPieces + (kPieces == 4 ? i ^ (row >> 1 & 3) : kPieces == 8 ? i ^ (row & 7) : i ^ ((row & 1) << 2));
+    }
 };
 
-template <int kBits, int kUnit>
-__device__ __forceinline__ void load_quad(Quad<kBits, kUnit>& q, const LinArgs& a, int tile, int u0, int g, int c) {
-    constexpr int kWords = Quad<kBits, kUnit>::kWords;
-    const moe_qtensor& W = a.W;
-    const int groups = W.in / W.group, row_words = W.in * kBits / 32;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t row = min(tile * kRows + g + 8 * r, W.out - 1);
-        const uint32_t* p = W.packed + row * row_words + c * kWords;
-#pragma unroll
-        for (int i = 0; i < kQuad; ++i) {
-            const uint32_t* pu = p + (int64_t)min(u0 + i, a.units - 1) * (4 * kWords);
-            if (kWords == 4) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(pu));
-                q.w[r][i][0] = v.x, q.w[r][i][kWords > 1 ? 1 : 0] = v.y;
-                q.w[r][i][kWords > 2 ? 2 : 0] = v.z, q.w[r][i][kWords > 3 ? 3 : 0] = v.w;
-            } else if (kWords == 2) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(pu));
-                q.w[r][i][0] = v.x, q.w[r][i][kWords > 1 ? 1 : 0] = v.y;
-            } else {
-                q.w[r][i][0] = __ldg(pu);
-            }
-        }
-        const uint16_t *ps = W.scales + row * groups, *pb = W.biases + row * groups;
-        if (a.vec) {
-            const uint2 s = __ldg(reinterpret_cast<const uint2*>(ps + u0)), b = __ldg(reinterpret_cast<const uint2*>(pb + u0));
-            q.s[r][0] = s.x, q.s[r][1] = s.y, q.b[r][0] = b.x, q.b[r][1] = b.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kQuad / 2; ++i) {
-                const int g0 = min(u0 + 2 * i, a.units - 1) * kUnit / W.group;
-                const int g1 = min(u0 + 2 * i + 1, a.units - 1) * kUnit / W.group;
-                q.s[r][i] = __ldg(ps + g0) | (uint32_t)__ldg(ps + g1) << 16;
-                q.b[r][i] = __ldg(pb + g0) | (uint32_t)__ldg(pb + g1) << 16;
-            }
-        }
-    }
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ float half_of(const uint32_t (&v)[kQuad / 2], int i) {
-    return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+__device__ __forceinline__ float half_of(const uint2& v, int i) {
+    const uint32_t w = i / 2 ? v.y : v.x;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
 }
 
 template <int kBits, int kUnit, int kNT>
 __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs a) {
-    using Q = Quad<kBits, kUnit>;
+    using S = Slot<kBits, kUnit>;
     constexpr int kParts = kUnit / 32;   // 16-byte pieces of x per lane and unit
     extern __shared__ __align__(16) unsigned char sm[];
-    const int K = a.W.in, tb = a.block, tb2 = (tb + 1) & ~1;
-    uint4* xs = reinterpret_cast<uint4*>(sm);                                      // [unit][part][token][quarter]
-    float* xsum = reinterpret_cast<float*>(sm + (size_t)tb * K * 2);               // [unit][tb2]
+    const moe_qtensor& W = a.W;
+    const int K = W.in, tb = a.block, tb2 = (tb + 1) & ~1, groups = W.in / W.group;
+    unsigned char* ring = sm + threadIdx.x / 32 * (S::kDepth * S::kBytes);         // this warp's
+    uint4* xs = reinterpret_cast<uint4*>(sm + kWarps * S::kDepth * S::kBytes);     // [unit][part][token][quarter]
+    float* xsum = reinterpret_cast<float*>(xs + (size_t)tb * K / 8);               // [unit][tb2]
     float* red = xsum + (size_t)a.units * tb2;                                     // [2][kWarps][kNT * 8][kRows]
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
     const int t0 = blockIdx.y * tb, nt = min(tb, a.T - t0);
-    const int tiles = (a.W.out + kRows - 1) / kRows, quads = (a.units + kQuad - 1) / kQuad;
+    const int tiles = (W.out + kRows - 1) / kRows, quads = (a.units + kQuad - 1) / kQuad;
     const int q0 = (int)((int64_t)quads * warp / kWarps), q1 = (int)((int64_t)quads * (warp + 1) / kWarps);
+    const int64_t row_bytes = (int64_t)K * kBits / 8;
+    const uint32_t sring = (uint32_t)__cvta_generic_to_shared(ring);
 
-    int tile = blockIdx.x, qi = q0;
-    Q cur, nxt;
-    if (q0 < q1) load_quad(cur, a, tile, q0 * kQuad, g, c);  // under way while x is staged
+    // copies run kDepth - 1 quads ahead, over the tiles' ends
+    int ctile = blockIdx.x, cq = q0, cslot = 0;
+    auto copy = [&]() {
+        if (ctile < tiles && cq < q1) {
+            const uint32_t dst = sring + cslot * S::kBytes;
+            const char* src = reinterpret_cast<const char*>(W.packed) + (int64_t)cq * (S::kPieces * 16);
+            const int left = (a.units - cq * kQuad) * S::kWords;  // pieces up to the row's end (a unit has kWords)
+#pragma unroll
+            for (int i = 0; i < S::kCopies; ++i) {
+                const int at = i * 32 + lane, row = at / S::kPieces, p = at % S::kPieces;
+                const int n = min(ctile * kRows + row, W.out - 1);
+                cp16(dst + S::piece(row, p) * 16, src + n * row_bytes + (p < left ? p * 16 : 0), p < left ? 16 : 0);
+            }
+            if (a.vec) {  // lane: row lane / 2, its scales or its biases
+                const int n = min(ctile * kRows + lane / 2, W.out - 1);
+                cp8(dst + kRows * S::kPieces * 16 + lane * 8,
+                    (lane & 1 ? W.biases : W.scales) + (int64_t)n * groups + cq * kQuad, 8);
+            }
+            if (++cq == q1) cq = q0, ctile += gridDim.x;
+            if (++cslot == S::kDepth) cslot = 0;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < S::kDepth - 1; ++i) copy();  // under way while x is staged
 
     // the block's tokens, in the order of the codes, and the sums of their units
     const int chunks = K / 8;
@@ -156,26 +157,64 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
         for (int u = tid; u < a.units; u += kThreads) xsum[u * tb2 + tb] = 0.0f;
     __syncthreads();
 
-    float y[kNT][4];
+    int slot = 0;
+    for (int tile = blockIdx.x, buf = 0; tile < tiles; tile += gridDim.x, buf ^= 1) {
+        float y[kNT][4];
 #pragma unroll
-    for (int n = 0; n < kNT; ++n)
+        for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[n][j] = 0.0f;
-
-    for (int buf = 0; tile < tiles; buf ^= 1) {
-        for (; qi < q1; ++qi) {
-            {  // the next loads: this tile's next units, or the next tile's first
-                const bool last = qi + 1 == q1;
-                const int nx = last ? tile + (int)gridDim.x : tile;
-                if (nx < tiles) load_quad(nxt, a, nx, (last ? q0 : qi + 1) * kQuad, g, c);
+            for (int j = 0; j < 4; ++j) y[n][j] = 0.0f;
+        for (int qi = q0; qi < q1; ++qi) {
+            uint2 sc[2], bi[2];  // scales and biases of the quad, bf16 pairs
+            if (!a.vec) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int64_t at = (int64_t)min(tile * kRows + g + 8 * r, W.out - 1) * groups;
+                    uint32_t e[2][kQuad];
+#pragma unroll
+                    for (int i = 0; i < kQuad; ++i) {
+                        const int gi = min(qi * kQuad + i, a.units - 1) * kUnit / W.group;
+                        e[0][i] = __ldg(W.scales + at + gi);
+                        e[1][i] = __ldg(W.biases + at + gi);
+                    }
+                    sc[r] = make_uint2(e[0][0] | e[0][1] << 16, e[0][2] | e[0][3] << 16);
+                    bi[r] = make_uint2(e[1][0] | e[1][1] << 16, e[1][2] | e[1][3] << 16);
+                }
+            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kDepth - 2) : "memory");
+            __syncwarp();
+            copy();  // into the slot of the quad before this one
+            const unsigned char* q = ring + slot * S::kBytes;
+            if (++slot == S::kDepth) slot = 0;
+            if (a.vec) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(q + kRows * S::kPieces * 16 + (g + 8 * r) * 16);
+                    sc[r] = make_uint2(v.x, v.y);
+                    bi[r] = make_uint2(v.z, v.w);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kQuad; ++i) {
                 const int u = qi * kQuad + i;
                 if (u >= a.units) break;
-                const float s0 = half_of(cur.s[0], i), s1 = half_of(cur.s[1], i);
-                const float kOff = kBits == 4 ? 128.0f : 128.0f * 17.0f;
-                const float b0 = fmaf(-kOff, s0, half_of(cur.b[0], i)), b1 = fmaf(-kOff, s1, half_of(cur.b[1], i));
+                uint32_t w[2][S::kWords];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const unsigned char* pw = q + S::piece(g + 8 * r, i * S::kWords + c * S::kWords / 4) * 16;
+                    if constexpr (S::kWords == 4) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(pw);
+                        w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+                    } else if constexpr (S::kWords == 2) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(pw + c % 2 * 8);
+                        w[r][0] = v.x, w[r][1] = v.y;
+                    } else {
+                        w[r][0] = *reinterpret_cast<const uint32_t*>(pw + c * 4);
+                    }
+                }
+                const float s0 = half_of(sc[0], i), s1 = half_of(sc[1], i);
+                constexpr float kOff = kBits == 4 ? 128.0f : 128.0f * 17.0f;
+                const float b0 = fmaf(-kOff, s0, half_of(bi[0], i)), b1 = fmaf(-kOff, s1, half_of(bi[1], i));
 #pragma unroll
                 for (int n = 0; n < kNT; ++n) {
                     float lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
@@ -183,15 +222,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                     for (int p = 0; p < kParts; ++p) {
                         uint4 x = make_uint4(0, 0, 0, 0);
                         if (8 * n + g < tb) x = xs[((int64_t)(u * kParts + p) * tb + 8 * n + g) * 4 + c];
-                        if (kBits == 4) {  // one word: eight codes
-                            const uint32_t w0 = cur.w[0][i][p % Q::kWords], w1 = cur.w[1][i][p % Q::kWords];
+                        if constexpr (kBits == 4) {  // one word: eight codes
+                            const uint32_t w0 = w[0][p], w1 = w[1][p];
                             mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 4), nib2(w1, 4), x.x, x.y);
                             mma16816(lo, nib2(w0, 8), nib2(w1, 8), nib2(w0, 12), nib2(w1, 12), x.z, x.w);
-                        } else {           // two words: eight codes, low and high nibbles
+                        } else {                     // two words: eight codes, low and high nibbles
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const int j = (2 * p + h) % Q::kWords;
-                                const uint32_t w0 = cur.w[0][i][j], w1 = cur.w[1][i][j];
+                                const uint32_t w0 = w[0][2 * p + h], w1 = w[1][2 * p + h];
                                 const uint32_t x0 = h ? x.z : x.x, x1 = h ? x.w : x.y;
                                 mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 8), nib2(w1, 8), x0, x1);
                                 mma16816(hi, nib2(w0, 4), nib2(w1, 4), nib2(w0, 12), nib2(w1, 12), x0, x1);
@@ -200,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                     }
                     float2 xt = make_float2(0.0f, 0.0f);
                     if (8 * n + 2 * c < tb) xt = *reinterpret_cast<const float2*>(&xsum[u * tb2 + 8 * n + 2 * c]);
-                    if (kBits == 8) {
+                    if constexpr (kBits == 8) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) lo[j] = fmaf(16.0f, hi[j], lo[j]);
                     }
@@ -210,27 +248,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                     y[n][3] += fmaf(s1, lo[3], b1 * xt.y);
                 }
             }
-            cur = nxt;
         }
         // the warps' parts, added in fixed order
         float* rb = red + buf * (kWarps * kNT * 8 * kRows);
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j)
                 rb[(warp * kNT * 8 + 8 * n + 2 * c + j % 2) * kRows + g + 8 * (j / 2)] = y[n][j];
-                y[n][j] = 0.0f;
-            }
         __syncthreads();
         for (int i = tid; i < nt * kRows; i += kThreads) {
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += rb[w * kNT * 8 * kRows + i];
             const int n = tile * kRows + i % kRows;
-            if (n < a.W.out) a.y[(int64_t)(t0 + i / kRows) * a.W.out + n] = f2bf16(v);
+            if (n < W.out) a.y[(int64_t)(t0 + i / kRows) * W.out + n] = f2bf16(v);
         }
-        tile += gridDim.x;
-        qi = q0;
     }
 }
 
@@ -271,21 +304,21 @@ int sm_count() {
     return n;
 }
 
-size_t codes_smem(const moe_qtensor& W, int unit, int tb, int nt) {
-    return (size_t)tb * W.in * 2 + (size_t)(W.in / unit) * ((tb + 1) & ~1) * 4 +
-           2u * kWarps * nt * 8 * kRows * sizeof(float);
+template <int kBits, int kUnit>
+size_t codes_smem(const moe_qtensor& W, int tb) {
+    using S = Slot<kBits, kUnit>;
+    return (size_t)kWarps * S::kDepth * S::kBytes + (size_t)tb * W.in * 2 +
+           (size_t)(W.in / kUnit) * ((tb + 1) & ~1) * 4 + 2u * kWarps * (tb > 8 ? 16 : 8) * kRows * sizeof(float);
 }
 
 template <int kBits, int kUnit, int kNT>
 cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
-    const size_t smem = codes_smem(a.W, kUnit, a.block, kNT);
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute((const void*)linear_codes_kernel<kBits, kUnit, kNT>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = codes_smem<kBits, kUnit>(a.W, a.block);
+    const cudaError_t e = cudaFuncSetAttribute((const void*)linear_codes_kernel<kBits, kUnit, kNT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int tiles = (a.W.out + kRows - 1) / kRows, across = (a.T + a.block - 1) / a.block;
-    const int room = std::max(1, (smem > 110 * 1024 ? 1 : 2) * sm_count() / across);
+    const int room = std::max(1, (smem > 113 * 1024 ? 1 : 2) * sm_count() / across);
     linear_codes_kernel<kBits, kUnit, kNT><<<dim3(std::min(tiles, room), across), kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
@@ -297,13 +330,20 @@ cudaError_t launch_unit(LinArgs a, cudaStream_t s) {
             ((uintptr_t)a.W.biases & 7) == 0;
     // as many tokens a block as one or two token tiles hold and shared memory takes
     int tb = std::min(a.T, 16);
-    while (tb > 1 && codes_smem(a.W, kUnit, tb, tb > 8 ? 2 : 1) > kMaxSmem) --tb;
+    while (tb > 1 && codes_smem<kBits, kUnit>(a.W, tb) > kMaxSmem) --tb;
     const int blocks = (a.T + tb - 1) / tb;
     a.block = (a.T + blocks - 1) / blocks;
     return a.block > 8 ? launch_codes<kBits, kUnit, 2>(a, s) : launch_codes<kBits, kUnit, 1>(a, s);
 }
 
 }  // namespace
+
+// Whether a row of x, and the ring beside it, fit in shared memory (from about 54,000 8-bit inputs on they do not).
+bool affine_codes_supported(const moe_qtensor& W) {
+    const size_t smem = W.group % 64 == 0 ? (W.bits == 4 ? codes_smem<4, 64>(W, 1) : codes_smem<8, 64>(W, 1))
+                                          : (W.bits == 4 ? codes_smem<4, 32>(W, 1) : codes_smem<8, 32>(W, 1));
+    return smem <= kMaxSmem;
+}
 
 cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T, uint16_t* y, cudaStream_t s) {
     LinArgs a;

@@ -48,7 +48,7 @@ CASES = [(1, 512, 2048, 4, 64), (1, 1, 32, 4, 32), (1, 17, 64, 4, 64), (2, 31, 9
          (5, 33, 128, 8, 64), (7, 64, 320, 4, 64), (8, 130, 2048, 4, 32), (9, 65, 1056, 8, 32), (13, 1003, 1056, 8, 32),
          (16, 48, 384, 4, 128), (17, 257, 512, 4, 64), (33, 128, 256, 4, 32), (64, 96, 640, 8, 64),
          (65, 72, 448, 4, 64), (100, 51, 96, 4, 32), (129, 136, 1024, 4, 64), (300, 264, 576, 8, 32),
-         (1, 40, 65536, 4, 64), (3, 24, 32768, 8, 64), (17, 16, 8192, 4, 64), (2, 4099, 256, 4, 64)]
+         (1, 40, 65536, 4, 64), (3, 24, 32768, 8, 64), (2, 24, 65536, 8, 64), (5, 19, 65536, 8, 32), (17, 16, 8192, 4, 64), (2, 4099, 256, 4, 64)]
 
 
 @pytest.mark.parametrize("T,N,K,bits,group", CASES)
