@@ -122,6 +122,32 @@ inline cudaError_t ensure_smem(const void* fn, size_t bytes, int& cached) {
     return e;
 }
 
+// The same for several devices in a process and for calls from several threads: `most` is a constant of the kernel, so
+// that setting it twice changes nothing.
+constexpr int kMaxDevices = 64;
+struct SmemLimit {
+    bool set[kMaxDevices] = {};
+    cudaError_t raise(const void* fn, size_t most) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || (dev < kMaxDevices && set[dev])) return e;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e == cudaSuccess && dev < kMaxDevices) set[dev] = true;
+        return e;
+    }
+};
+
+// Multiprocessors of the current device.
+inline int device_sms() {
+    static int known[kMaxDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < kMaxDevices && known[dev] > 0) return known[dev];
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (dev < kMaxDevices) known[dev] = n;
+    return n;
+}
+
 // ------------------------------------------------------------- fused decode
 #define MOEQ_DECODE_MAX_TOKENS 8
 #define MOEQ_DECODE_MAX_JOBS 32

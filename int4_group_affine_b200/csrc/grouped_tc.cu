@@ -739,16 +739,12 @@ bool encode_mn(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64
 
 template <int kDir, int kF16, int kCta>
 cudaError_t launch_cta(const TcGmm& p, int64_t tiles, cudaStream_t s) {
-    int dev = 0, nsm = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute((const void*)gmm_tc_kernel<kDir, kF16, kCta>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<kDir, kCta>::smem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise((const void*)gmm_tc_kernel<kDir, kF16, kCta>, Ring<kDir, kCta>::smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, nsm / kCta) * kCta);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, device_sms() / kCta) * kCta);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Ring<kDir, kCta>::smem;
     cfg.stream = s;

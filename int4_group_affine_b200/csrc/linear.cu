@@ -15,11 +15,11 @@
 // A dot product does not mind the order of its terms, so a lane takes the k that lie together in
 // its words: lane (row r, quarter c) loads a unit's quarter c (a unit is the 64 or 32 inputs that
 // one scale covers at least), and the rows of x are staged in shared memory in that order, with the
-// sum of each unit beside them.  A block holds 16 matrix rows; its eight warps split the units and
-// add their partial sums in shared memory in fixed order.  Blocks stay (two per SM) and walk the
-// matrix, each warp's next loads under way while it multiplies: with x staged once per block,
-// shared memory and the tensor cores do little, and the loads in flight (16 warps x 4 KB per SM)
-// cover the memory's latency.
+// sum of each unit beside them.  Tall matrices give every warp tiles of its own; where there are too
+// few tiles, two, four or eight warps of a block split a tile's units and add their partial sums in
+// shared memory in fixed order.  Blocks stay (two per SM) and walk the matrix, each warp with a ring
+// of its own that asynchronous copies fill one to three quads (four units of a tile) ahead: x is
+// staged once per block, and the copies in flight cover the memory's latency.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,21 +28,34 @@ namespace moeq {
 namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kRows = 16;                        // matrix rows of a tile
 constexpr int kQuad = 4;                         // units loaded together
 constexpr size_t kMaxSmem = 226 * 1024;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
         "%2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same from zero.
+__device__ __forceinline__ void mma16816_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+        "%10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 
 // Nibbles j and j + 4 of a word (j = shift / 4) as the bf16 pair {128 + q_j, 128 + q_j+4}.
-__device__ __forceinline__ uint32_t nib2(uint32_t w, int shift) { return ((w >> shift) & 0x000F000Fu) | 0x43004300u; }
+// (one three-input instruction: left to itself the compiler takes two)
+__device__ __forceinline__ uint32_t nib2(uint32_t w, int shift) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> shift), "r"(0x000F000Fu), "r"(0x43004300u));
+    return r;
+}
 
 // Eight bf16 values in the pair order in which the codes leave their words: a 4-bit word gives
 // (0, 4) (1, 5) (2, 6) (3, 7); the two 8-bit words give (0, 2) (1, 3), (4, 6) (5, 7).
@@ -62,18 +75,20 @@ struct LinArgs {
     int T;        // tokens
     int block;    // tokens of a block (<= 8 kNT)
     int units;    // per row
+    int split;    // warps that share a tile: 1, 2, 4 or 8
     int vec;      // scales and biases of four units can be loaded together
 };
 
-// A quad's words of a tile's 16 rows in a warp's ring, in 16-byte pieces that change places by row so that the
+// A quad's words of a tile's rows in a warp's ring, in 16-byte pieces that change places by row so that the
 // fragment loads (a unit's quarters of eight rows at once) meet no two in one bank.
-template <int kBits, int kUnit>
+template <int kBits, int kUnit, int kMT>
 struct Slot {
+    static constexpr int kRows = 16 * kMT;                         // matrix rows of a tile
     static constexpr int kWords = kUnit * kBits / 128;             // words of a unit's quarter: 1, 2 or 4
     static constexpr int kPieces = kQuad * kWords;                 // 16-byte pieces of a row: 4, 8 or 16
     static constexpr int kCopies = kRows * kPieces / 32;           // per lane
     static constexpr int kBytes = kRows * kPieces * 16 + 2 * kRows * kQuad * 2;  // and the scales and biases
-    static constexpr int kDepth = kWords == 4 ? 3 : 4;             // quads in the ring
+    static constexpr int kDepth = kMT == 2 ? 2 : kWords == 4 ? 3 : 4;            // quads in the ring
     __device__ static __forceinline__ int piece(int row, int i) {
         return row * kPieces + (kPieces == 4 ? i ^ (row >> 1 & 3) : kPieces == 8 ? i ^ (row & 7) : i ^ ((row & 1) << 2));
     }
@@ -86,48 +101,82 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t byt
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
 __device__ __forceinline__ float half_of(const uint2& v, int i) {
     const uint32_t w = i / 2 ? v.y : v.x;
     return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
 }
 
-template <int kBits, int kUnit, int kNT>
+template <int kBits, int kUnit, int kNT, int kMT>
 __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs a) {
-    using S = Slot<kBits, kUnit>;
+    using S = Slot<kBits, kUnit, kMT>;
     constexpr int kParts = kUnit / 32;   // 16-byte pieces of x per lane and unit
+    constexpr int kRows = S::kRows, kRed = kNT * 8 * kRows;
     extern __shared__ __align__(16) unsigned char sm[];
     const moe_qtensor& W = a.W;
     const int K = W.in, tb = a.block, tb2 = (tb + 1) & ~1, groups = W.in / W.group;
-    unsigned char* ring = sm + threadIdx.x / 32 * (S::kDepth * S::kBytes);         // this warp's
-    uint4* xs = reinterpret_cast<uint4*>(sm + kWarps * S::kDepth * S::kBytes);     // [unit][part][token][quarter]
-    float* xsum = reinterpret_cast<float*>(xs + (size_t)tb * K / 8);               // [unit][tb2]
-    float* red = xsum + (size_t)a.units * tb2;                                     // [2][kWarps][kNT * 8][kRows]
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
+    unsigned char* ring = sm + warp * (S::kDepth * S::kBytes);                     // this warp's
+    // x: [unit][token][quarter and part], a unit's 16-byte pieces of two neighbouring tokens in opposite halves (else
+    // they would share banks); then a block of zeros that the lanes of tokens past the last read
+    uint4* xs = reinterpret_cast<uint4*>(sm + kWarps * S::kDepth * S::kBytes);
+    const int xunit = tb * 4 * kParts;                                             // pieces of a unit
+    uint4* zeros = xs + (size_t)a.units * xunit;
+    float* xsum = reinterpret_cast<float*>(zeros + 4 * kParts);                    // [unit][tb2], then zeros
+    float* red = xsum + (size_t)a.units * tb2 + 8;                                     // [2][kWarps][kRed]
     const int t0 = blockIdx.y * tb, nt = min(tb, a.T - t0);
     const int tiles = (W.out + kRows - 1) / kRows, quads = (a.units + kQuad - 1) / kQuad;
-    const int q0 = (int)((int64_t)quads * warp / kWarps), q1 = (int)((int64_t)quads * (warp + 1) / kWarps);
-    const int64_t row_bytes = (int64_t)K * kBits / 8;
+    // the block's warps: kWarps / split tiles at a time, `split` of them to a tile's units
+    const int split = a.split, part = warp % split, across = kWarps / split;
+    const int q0 = (int)((int64_t)quads * part / split), q1 = (int)((int64_t)quads * (part + 1) / split);
+    const int first = blockIdx.x * across + warp / split, stride = gridDim.x * across;
+    const int row_bytes = K * kBits / 8;
     const uint32_t sring = (uint32_t)__cvta_generic_to_shared(ring);
 
-    // copies run kDepth - 1 quads ahead, over the tiles' ends
-    int ctile = blockIdx.x, cq = q0, cslot = 0;
+    // copies run kDepth - 1 quads ahead, over the tiles' ends; a lane's pieces are kStep rows apart
+    constexpr int kStep = 32 / S::kPieces;
+    const int crow = lane / S::kPieces, cp = lane % S::kPieces;
+    int ctile = first, cq = q0, cslot = 0;
     auto copy = [&]() {
         if (ctile < tiles && cq < q1) {
             const uint32_t dst = sring + cslot * S::kBytes;
-            const char* src = reinterpret_cast<const char*>(W.packed) + (int64_t)cq * (S::kPieces * 16);
+            const char* src = reinterpret_cast<const char*>(W.packed) + (int64_t)ctile * kRows * row_bytes +
+                              cq * (S::kPieces * 16);
             const int left = (a.units - cq * kQuad) * S::kWords;  // pieces up to the row's end (a unit has kWords)
+            const int last = W.out - 1 - ctile * kRows;            // the tile's last row
+            if (left >= S::kPieces && last >= kRows - 1) {
+                const char* p = src + crow * row_bytes + cp * 16;
 #pragma unroll
-            for (int i = 0; i < S::kCopies; ++i) {
-                const int at = i * 32 + lane, row = at / S::kPieces, p = at % S::kPieces;
-                const int n = min(ctile * kRows + row, W.out - 1);
-                cp16(dst + S::piece(row, p) * 16, src + n * row_bytes + (p < left ? p * 16 : 0), p < left ? 16 : 0);
+                for (int i = 0; i < S::kCopies; ++i, p += kStep * row_bytes)
+                    cp16(dst + S::piece(i * kStep + crow, cp) * 16, p, 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < S::kCopies; ++i)
+                    cp16(dst + S::piece(i * kStep + crow, cp) * 16,
+                         src + min(i * kStep + crow, last) * row_bytes + (cp < left ? cp * 16 : 0), cp < left ? 16 : 0);
             }
-            if (a.vec) {  // lane: row lane / 2, its scales or its biases
-                const int n = min(ctile * kRows + lane / 2, W.out - 1);
-                cp8(dst + kRows * S::kPieces * 16 + lane * 8,
-                    (lane & 1 ? W.biases : W.scales) + (int64_t)n * groups + cq * kQuad, 8);
+            if (a.vec) {  // lane: row lane / 2 (and 16 further), its scales or its biases
+                const uint16_t* sb = (lane & 1 ? W.biases : W.scales) + (int64_t)ctile * kRows * groups + cq * kQuad;
+#pragma unroll
+                for (int m = 0; m < kMT; ++m)
+                    cp8(dst + kRows * S::kPieces * 16 + (m * 32 + lane) * 8, sb + min(m * 16 + lane / 2, last) * groups, 8);
             }
-            if (++cq == q1) cq = q0, ctile += gridDim.x;
+            if (++cq == q1) cq = q0, ctile += stride;
             if (++cslot == S::kDepth) cslot = 0;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -149,26 +198,51 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
         for (int o = 1; o < kUnit / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (t < tb) {
             const int u = ch / (kUnit / 8), in = ch % (kUnit / 8);
-            xs[((int64_t)(u * kParts + in % kParts) * tb + t) * 4 + in / kParts] = code_order<kBits>(v);
+            xs[u * xunit + t * 4 * kParts + ((in % kParts) ^ (kParts == 2 ? t & 1 : 0)) * 4 + in / kParts] = code_order<kBits>(v);
             if (in == 0) xsum[u * tb2 + t] = s;
         }
     }
     if (tb < tb2)
         for (int u = tid; u < a.units; u += kThreads) xsum[u * tb2 + tb] = 0.0f;
+    if (tid < 4 * kParts) zeros[tid] = make_uint4(0, 0, 0, 0);
+    if (tid < 8) xsum[a.units * tb2 + tid] = 0.0f;
     __syncthreads();
+    // where this lane's pieces of x and sums start, and how far apart its units are (shared memory addresses: the
+    // integer pipe that unpacks the codes has no room for address arithmetic)
+    uint32_t xp[kNT][kParts], sp[kNT], xstep[kNT], sstep[kNT];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+        const int t = 8 * n + g;
+        xstep[n] = t < tb ? xunit * 16 : 0;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+            xp[n][p] = (uint32_t)__cvta_generic_to_shared(t < tb ? xs + t * 4 * kParts : zeros) +
+                       ((p ^ (kParts == 2 ? t & 1 : 0)) * 4 + c) * 16;
+        const bool in = 8 * n + 2 * c < tb;
+        sstep[n] = in ? tb2 * 4 : 0;
+        sp[n] = (uint32_t)__cvta_generic_to_shared(xsum + (in ? 8 * n + 2 * c : a.units * tb2));
+    }
+    uint32_t wp[kQuad];  // and its quarter of a unit's words within a slot, for the first of its rows
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i)
+        wp[i] = S::piece(g, i * S::kWords + c * S::kWords / 4) * 16 + (S::kWords == 4 ? 0 : S::kWords == 2 ? c % 2 * 8 : c * 4);
+    const uint32_t cp_s = kRows * S::kPieces * 16 + g * 16;
 
     int slot = 0;
-    for (int tile = blockIdx.x, buf = 0; tile < tiles; tile += gridDim.x, buf ^= 1) {
-        float y[kNT][4];
+    // (warps that share tiles go as many rounds as the block's first one)
+    for (int tile = first, buf = 0; (split == 1 ? tile : tile - warp / split) < tiles; tile += stride, buf ^= 1) {
+        float y[kMT][kNT][4];
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+        for (int m = 0; m < kMT; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[n][j] = 0.0f;
-        for (int qi = q0; qi < q1; ++qi) {
-            uint2 sc[2], bi[2];  // scales and biases of the quad, bf16 pairs
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[m][n][j] = 0.0f;
+        for (int qi = q0; qi < q1 && tile < tiles; ++qi) {
+            uint2 sc[kMT][2], bi[kMT][2];  // scales and biases of the quad, bf16 pairs
             if (!a.vec) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < 2 * kMT; ++r) {
                     const int64_t at = (int64_t)min(tile * kRows + g + 8 * r, W.out - 1) * groups;
                     uint32_t e[2][kQuad];
 #pragma unroll
@@ -177,92 +251,122 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                         e[0][i] = __ldg(W.scales + at + gi);
                         e[1][i] = __ldg(W.biases + at + gi);
                     }
-                    sc[r] = make_uint2(e[0][0] | e[0][1] << 16, e[0][2] | e[0][3] << 16);
-                    bi[r] = make_uint2(e[1][0] | e[1][1] << 16, e[1][2] | e[1][3] << 16);
+                    sc[r / 2][r % 2] = make_uint2(e[0][0] | e[0][1] << 16, e[0][2] | e[0][3] << 16);
+                    bi[r / 2][r % 2] = make_uint2(e[1][0] | e[1][1] << 16, e[1][2] | e[1][3] << 16);
                 }
             }
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kDepth - 2) : "memory");
             __syncwarp();
             copy();  // into the slot of the quad before this one
-            const unsigned char* q = ring + slot * S::kBytes;
+            const uint32_t q = sring + slot * S::kBytes;
             if (++slot == S::kDepth) slot = 0;
             if (a.vec) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(q + kRows * S::kPieces * 16 + (g + 8 * r) * 16);
-                    sc[r] = make_uint2(v.x, v.y);
-                    bi[r] = make_uint2(v.z, v.w);
+                for (int r = 0; r < 2 * kMT; ++r) {
+                    const uint4 v = lds128(q + cp_s + 8 * r * 16);
+                    sc[r / 2][r % 2] = make_uint2(v.x, v.y);
+                    bi[r / 2][r % 2] = make_uint2(v.z, v.w);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kQuad; ++i) {
                 const int u = qi * kQuad + i;
                 if (u >= a.units) break;
-                uint32_t w[2][S::kWords];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const unsigned char* pw = q + S::piece(g + 8 * r, i * S::kWords + c * S::kWords / 4) * 16;
-                    if constexpr (S::kWords == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(pw);
-                        w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-                    } else if constexpr (S::kWords == 2) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(pw + c % 2 * 8);
-                        w[r][0] = v.x, w[r][1] = v.y;
-                    } else {
-                        w[r][0] = *reinterpret_cast<const uint32_t*>(pw + c * 4);
-                    }
-                }
-                const float s0 = half_of(sc[0], i), s1 = half_of(sc[1], i);
-                constexpr float kOff = kBits == 4 ? 128.0f : 128.0f * 17.0f;
-                const float b0 = fmaf(-kOff, s0, half_of(bi[0], i)), b1 = fmaf(-kOff, s1, half_of(bi[1], i));
+                uint4 x[kNT][kParts];
+                float2 xt[kNT];
 #pragma unroll
                 for (int n = 0; n < kNT; ++n) {
-                    float lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (8 * n + g < tb) x = xs[((int64_t)(u * kParts + p) * tb + 8 * n + g) * 4 + c];
-                        if constexpr (kBits == 4) {  // one word: eight codes
-                            const uint32_t w0 = w[0][p], w1 = w[1][p];
-                            mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 4), nib2(w1, 4), x.x, x.y);
-                            mma16816(lo, nib2(w0, 8), nib2(w1, 8), nib2(w0, 12), nib2(w1, 12), x.z, x.w);
-                        } else {                     // two words: eight codes, low and high nibbles
+                    for (int p = 0; p < kParts; ++p) x[n][p] = lds128(xp[n][p] + u * xstep[n]);
+                    const uint2 v = lds64(sp[n] + u * sstep[n]);
+                    xt[n] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+                }
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t w0 = w[0][2 * p + h], w1 = w[1][2 * p + h];
-                                const uint32_t x0 = h ? x.z : x.x, x1 = h ? x.w : x.y;
-                                mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 8), nib2(w1, 8), x0, x1);
-                                mma16816(hi, nib2(w0, 4), nib2(w1, 4), nib2(w0, 12), nib2(w1, 12), x0, x1);
-                            }
+                for (int m = 0; m < kMT; ++m) {
+                    uint32_t w[2][S::kWords];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t pw = q + wp[i] + (16 * m + 8 * r) * S::kPieces * 16;
+                        if constexpr (S::kWords == 4) {
+                            const uint4 v = lds128(pw);
+                            w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+                        } else if constexpr (S::kWords == 2) {
+                            const uint2 v = lds64(pw);
+                            w[r][0] = v.x, w[r][1] = v.y;
+                        } else {
+                            w[r][0] = lds32(pw);
                         }
                     }
-                    float2 xt = make_float2(0.0f, 0.0f);
-                    if (8 * n + 2 * c < tb) xt = *reinterpret_cast<const float2*>(&xsum[u * tb2 + 8 * n + 2 * c]);
-                    if constexpr (kBits == 8) {
+                    const float s0 = half_of(sc[m][0], i), s1 = half_of(sc[m][1], i);
+                    constexpr float kOff = kBits == 4 ? 128.0f : 128.0f * 17.0f;
+                    const float b0 = fmaf(-kOff, s0, half_of(bi[m][0], i)), b1 = fmaf(-kOff, s1, half_of(bi[m][1], i));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) lo[j] = fmaf(16.0f, hi[j], lo[j]);
+                    for (int n = 0; n < kNT; ++n) {
+                        float lo[4], hi[4];
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) {
+                            const uint4 v = x[n][p];
+                            if constexpr (kBits == 4) {  // one word: eight codes
+                                const uint32_t w0 = w[0][p], w1 = w[1][p];
+                                if (p == 0) mma16816_0(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 4), nib2(w1, 4), v.x, v.y);
+                                else mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 4), nib2(w1, 4), v.x, v.y);
+                                mma16816(lo, nib2(w0, 8), nib2(w1, 8), nib2(w0, 12), nib2(w1, 12), v.z, v.w);
+                            } else {                     // two words: eight codes, low and high nibbles
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t w0 = w[0][2 * p + h], w1 = w[1][2 * p + h];
+                                    const uint32_t x0 = h ? v.z : v.x, x1 = h ? v.w : v.y;
+                                    if (p == 0 && h == 0) {
+                                        mma16816_0(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 8), nib2(w1, 8), x0, x1);
+                                        mma16816_0(hi, nib2(w0, 4), nib2(w1, 4), nib2(w0, 12), nib2(w1, 12), x0, x1);
+                                    } else {
+                                        mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 8), nib2(w1, 8), x0, x1);
+                                        mma16816(hi, nib2(w0, 4), nib2(w1, 4), nib2(w0, 12), nib2(w1, 12), x0, x1);
+                                    }
+                                }
+                            }
+                        }
+                        if constexpr (kBits == 8) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) lo[j] = fmaf(16.0f, hi[j], lo[j]);
+                        }
+                        float(&o)[4] = y[m][n];
+                        o[0] = fmaf(s0, lo[0], fmaf(b0, xt[n].x, o[0]));
+                        o[1] = fmaf(s0, lo[1], fmaf(b0, xt[n].y, o[1]));
+                        o[2] = fmaf(s1, lo[2], fmaf(b1, xt[n].x, o[2]));
+                        o[3] = fmaf(s1, lo[3], fmaf(b1, xt[n].y, o[3]));
                     }
-                    y[n][0] += fmaf(s0, lo[0], b0 * xt.x);
-                    y[n][1] += fmaf(s0, lo[1], b0 * xt.y);
-                    y[n][2] += fmaf(s1, lo[2], b1 * xt.x);
-                    y[n][3] += fmaf(s1, lo[3], b1 * xt.y);
                 }
             }
         }
+        if (split == 1) {
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = 8 * n + 2 * c + j % 2, o = tile * kRows + 16 * m + g + 8 * (j / 2);
+                        if (t < nt && o < W.out) a.y[(int64_t)(t0 + t) * W.out + o] = f2bf16(y[m][n][j]);
+                    }
+            continue;
+        }
         // the warps' parts, added in fixed order
-        float* rb = red + buf * (kWarps * kNT * 8 * kRows);
+        float* rb = red + buf * (kWarps * kRed);
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+        for (int m = 0; m < kMT; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                rb[(warp * kNT * 8 + 8 * n + 2 * c + j % 2) * kRows + g + 8 * (j / 2)] = y[n][j];
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    rb[warp * kRed + (8 * n + 2 * c + j % 2) * kRows + 16 * m + g + 8 * (j / 2)] = y[m][n][j];
         __syncthreads();
-        for (int i = tid; i < nt * kRows; i += kThreads) {
+        for (int i = tid; i < across * nt * kRows; i += kThreads) {
+            const int at = i / (nt * kRows), in = i % (nt * kRows);
+            const int n = (tile - warp / split + at) * kRows + in % kRows;
             float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += rb[w * kNT * 8 * kRows + i];
-            const int n = tile * kRows + i % kRows;
-            if (n < W.out) a.y[(int64_t)(t0 + i / kRows) * W.out + n] = f2bf16(v);
+            for (int w = 0; w < split; ++w) v += rb[(at * split + w) * kRed + in];
+            if (n < W.out) a.y[(int64_t)(t0 + in / kRows) * W.out + n] = f2bf16(v);
         }
     }
 }
@@ -297,29 +401,36 @@ __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-}
-
 template <int kBits, int kUnit>
-size_t codes_smem(const moe_qtensor& W, int tb) {
-    using S = Slot<kBits, kUnit>;
-    return (size_t)kWarps * S::kDepth * S::kBytes + (size_t)tb * W.in * 2 +
-           (size_t)(W.in / kUnit) * ((tb + 1) & ~1) * 4 + 2u * kWarps * (tb > 8 ? 16 : 8) * kRows * sizeof(float);
+size_t codes_smem(const moe_qtensor& W, int tb, int mt) {
+    const size_t ring = mt == 2 ? Slot<kBits, kUnit, 2>::kDepth * Slot<kBits, kUnit, 2>::kBytes
+                                : Slot<kBits, kUnit, 1>::kDepth * Slot<kBits, kUnit, 1>::kBytes;
+    return kWarps * ring + (size_t)tb * W.in * 2 + kUnit * 2 + (size_t)(W.in / kUnit) * ((tb + 1) & ~1) * 4 + 32 +
+           2u * kWarps * (tb > 8 ? 16 : 8) * 16 * mt * sizeof(float);
 }
 
-template <int kBits, int kUnit, int kNT>
+template <int kBits, int kUnit, int kNT, int kMT>
 cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
-    const size_t smem = codes_smem<kBits, kUnit>(a.W, a.block);
-    const cudaError_t e = cudaFuncSetAttribute((const void*)linear_codes_kernel<kBits, kUnit, kNT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = codes_smem<kBits, kUnit>(a.W, a.block, kMT);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise((const void*)linear_codes_kernel<kBits, kUnit, kNT, kMT>, kMaxSmem);
     if (e != cudaSuccess) return e;
+    constexpr int kRows = 16 * kMT;
     const int tiles = (a.W.out + kRows - 1) / kRows, across = (a.T + a.block - 1) / a.block;
-    const int room = std::max(1, (smem > 113 * 1024 ? 1 : 2) * sm_count() / across);
-    linear_codes_kernel<kBits, kUnit, kNT><<<dim3(std::min(tiles, room), across), kThreads, smem, s>>>(a);
+    const int room = std::max(1, (smem > 113 * 1024 ? 1 : 2) * device_sms() / across);
+    // The warps that share a tile (1, 2, 4 or 8): the fewest rounds' worth of quads a warp walks, a round of shared
+    // tiles costing about a quarter of a quad more for adding the parts up.  (2048 inputs, one token: 131072 outputs
+    // take 36.6 us with four warps, 39.6 with one, whose second round is three quarters empty; 512 outputs need all
+    // eight.)
+    const int quads = (a.units + kQuad - 1) / kQuad;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= kWarps && s <= std::max(quads, 1); s *= 2) {
+        const int64_t at_once = (int64_t)room * (kWarps / s);
+        const int64_t cost = (tiles + at_once - 1) / at_once * (4 * ((quads + s - 1) / s) + (s > 1));
+        if (cost < best) best = cost, a.split = s;
+    }
+    const int per = kWarps / a.split, want = (tiles + per - 1) / per;
+    linear_codes_kernel<kBits, kUnit, kNT, kMT><<<dim3(std::min(want, room), across), kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -330,18 +441,22 @@ cudaError_t launch_unit(LinArgs a, cudaStream_t s) {
             ((uintptr_t)a.W.biases & 7) == 0;
     // as many tokens a block as one or two token tiles hold and shared memory takes
     int tb = std::min(a.T, 16);
-    while (tb > 1 && codes_smem<kBits, kUnit>(a.W, tb) > kMaxSmem) --tb;
+    while (tb > 1 && codes_smem<kBits, kUnit>(a.W, tb, 1) > kMaxSmem) --tb;
     const int blocks = (a.T + tb - 1) / tb;
     a.block = (a.T + blocks - 1) / blocks;
-    return a.block > 8 ? launch_codes<kBits, kUnit, 2>(a, s) : launch_codes<kBits, kUnit, 1>(a, s);
+    if (a.block > 8) return launch_codes<kBits, kUnit, 2, 1>(a, s);
+    // tall matrices: two row tiles a warp share the loads of x (and two blocks still fit an SM)
+    if (a.W.out >= 32 * 2 * kWarps * device_sms() && codes_smem<kBits, kUnit>(a.W, a.block, 2) <= 113 * 1024)
+        return launch_codes<kBits, kUnit, 1, 2>(a, s);
+    return launch_codes<kBits, kUnit, 1, 1>(a, s);
 }
 
 }  // namespace
 
 // Whether a row of x, and the ring beside it, fit in shared memory (from about 54,000 8-bit inputs on they do not).
 bool affine_codes_supported(const moe_qtensor& W) {
-    const size_t smem = W.group % 64 == 0 ? (W.bits == 4 ? codes_smem<4, 64>(W, 1) : codes_smem<8, 64>(W, 1))
-                                          : (W.bits == 4 ? codes_smem<4, 32>(W, 1) : codes_smem<8, 32>(W, 1));
+    const size_t smem = W.group % 64 == 0 ? (W.bits == 4 ? codes_smem<4, 64>(W, 1, 1) : codes_smem<8, 64>(W, 1, 1))
+                                          : (W.bits == 4 ? codes_smem<4, 32>(W, 1, 1) : codes_smem<8, 32>(W, 1, 1));
     return smem <= kMaxSmem;
 }
 
@@ -357,7 +472,7 @@ cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T,
 
 cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s) {
     const int64_t pieces = (int64_t)W.out * W.in / 8, want = (pieces + 255) / 256;
-    const unsigned blocks = (unsigned)std::min<int64_t>(want, (int64_t)sm_count() * 8);
+    const unsigned blocks = (unsigned)std::min<int64_t>(want, (int64_t)device_sms() * 8);
     if (W.bits == 4) dequant16_kernel<4><<<blocks, 256, 0, s>>>(W, pieces, reinterpret_cast<uint4*>(out));
     else dequant16_kernel<8><<<blocks, 256, 0, s>>>(W, pieces, reinterpret_cast<uint4*>(out));
     return cudaGetLastError();
