@@ -68,6 +68,7 @@ template <int kDir, int kF16>
 __global__ void __launch_bounds__(kThreads) gmm_any_kernel(const GmmArgs a) {
     __shared__ __align__(16) uint16_t sA[kT][kPitch], sB[kT][kPitch];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g8 = lane / 4, c4 = lane % 4;
+    grid_wait();
     if (blockIdx.x == 0) (void)gmm_check_offsets(a, tid, kThreads);
 
     // the tile: group, output rows [i0, I) and columns [j0, J), terms [0, S)
@@ -174,9 +175,8 @@ cudaError_t launch_any(const GmmArgs& a, int f16, cudaStream_t s) {
     const int64_t tiles = kDir == kGmmDw ? (int64_t)a.G * ((a.N + kT - 1) / kT) * jt
                                          : ((int64_t)a.M / kT + (a.off ? a.G : 1)) * jt;
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if (f16) gmm_any_kernel<kDir, 1><<<(unsigned)tiles, kThreads, 0, s>>>(a);
-    else gmm_any_kernel<kDir, 0><<<(unsigned)tiles, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(f16 ? gmm_any_kernel<kDir, 1> : gmm_any_kernel<kDir, 0>, dim3((unsigned)tiles), kThreads, 0, 1, s,
+                            a);
 }
 
 }  // namespace

@@ -31,7 +31,6 @@
 // the other (a fixed order).
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
-#include <string.h>
 
 #include <algorithm>
 
@@ -59,13 +58,14 @@ struct Ring {
     static constexpr int stages = kCta == 2 ? 6 : 4;
     static constexpr int bytes = kABytes + kCols / kCta * 128;
     static constexpr size_t smem = 1024 + stages * bytes + outs * kEpi * kOutBytes;
-    static_assert(smem + 1024 <= 227 * 1024, "shared memory");
+    static_assert(smem + (kDir == kGmmDw ? 1024 : 10 * 1024) <= 227 * 1024, "shared memory");
 };
 
 struct TcGmm {
     CUtensorMap tma;     // the lanes' operand
     CUtensorMap tmb[4];  // the columns' operand: forward, dx in boxes of 16, 32, 64 and 128 rows; dw [0]
     CUtensorMap tmo;     // dw: the output, in boxes of 32 rows x 128 bytes
+    int table;           // forward, dx: the groups fit the block's table
     int wide_a, wide_b;  // an MN-major operand whose whole tile is one box (see encode_mn)
     GmmArgs a;
 };
@@ -80,6 +80,60 @@ struct Tile {
     int terms;     // length of the sum
     int row0;      // dw: first row of the group
 };
+
+// The groups' tiles, worked out once a block for up to kTable groups whose offsets are in order (others walk the
+// offsets as they go): finding a tile's group takes two looks instead of one for every 32 groups before it.
+constexpr int kTable = 1024;
+struct Table {
+    int off[kTable + 1];
+    int upto[kTable];         // tiles up to and with a group, counted from its window of 32 groups
+    int before[kTable / 32];  // tiles before a window
+};
+
+// Fills the table (all threads of the block).
+template <int kThreads>
+__device__ __forceinline__ void fill_table(Table& tb, const GmmArgs& a, int across, int tid) {
+    const int warp = tid / 32, lane = tid % 32, windows = (a.G + 31) / 32;
+    for (int i = tid; i <= a.G; i += kThreads) tb.off[i] = __ldg(a.off + i);
+    __syncthreads();
+    for (int w = warp; w < windows; w += kThreads / 32) {
+        const int g = 32 * w + lane;
+        int t = g < a.G ? (tb.off[g + 1] - tb.off[g] + kCols - 1) / kCols * across : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += v;
+        }
+        tb.upto[g] = t;
+        if (lane == 31) tb.before[w] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int t = lane < windows ? tb.before[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += v;
+        }
+        t = __shfl_up_sync(0xffffffffu, t, 1);
+        if (lane < windows) tb.before[lane] = lane ? t : 0;
+    }
+    __syncthreads();
+}
+
+// The group that owns `tile` (a warp; -1: none), its rows and the tile's index within it.
+__device__ __forceinline__ int find_in(const Table& tb, int G, int64_t tile, int lane, GmmRows* rows, int* within) {
+    const int windows = (G + 31) / 32;
+    const uint32_t m = __ballot_sync(0xffffffffu, lane < windows && tile >= tb.before[min(lane, windows - 1)]);
+    const int w = 31 - __clz(m), rest = (int)(tile - tb.before[w]);  // (window 0 begins with tile 0)
+    const int upto = tb.upto[32 * w + lane];
+    const uint32_t in = __ballot_sync(0xffffffffu, rest < upto);
+    if (in == 0) return -1;
+    const int l = __ffs(in) - 1, g = 32 * w + l;
+    *rows = GmmRows{tb.off[g], tb.off[g + 1]};
+    *within = rest - (l > 0 ? __shfl_sync(0xffffffffu, upto, l - 1) : 0);
+    return g;
+}
 
 // n / d and n % d for small n (a quotient below 2^22), without the integer division's hundred instructions.
 struct Quot {
@@ -100,6 +154,7 @@ struct Schedule {
     static constexpr int kUp = 16 * kCta;  // what the instruction's width is a multiple of
     GmmWalk walk;
     GmmRows rows;                          // (dw: as read, ahead of the tile)
+    const Table* table;                    // forward, dx: or NULL
     bool good;
     int g = -1, across, left;              // left: tiles (forward, dx: of this group) from this one on
     int within, step, step_g;              // dw: tile within the group, and the stride in groups and tiles
@@ -107,8 +162,9 @@ struct Schedule {
     int64_t tile;
     float inv;
 
-    __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane, bool good_) {
+    __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane, bool good_, const Table* table_) {
         good = good_;
+        table = table_;
         if (kDir == kGmmDw) {
             across = (a.K + kCols - 1) / kCols;
             left = (a.N + kTileLanes - 1) / kTileLanes * across;  // tiles of a group
@@ -155,15 +211,19 @@ struct Schedule {
             }
         } else {
             if (left <= 0) {  // another group
-                int64_t w;
-                g = walk.find(a, lane, tile, kCols, across, &rows, &w);
+                if (table) {
+                    g = find_in(*table, a.G, tile, lane, &rows, &within);
+                } else {
+                    int64_t w = 0;
+                    g = walk.find(a, lane, tile, kCols, across, &rows, &w);
+                    within = (int)w;
+                }
                 t.g = g;
                 if (g < 0) return t;
                 const int count = rows.end - rows.begin;
                 parts = (count + kCols - 1) / kCols;
                 width = parts == 1 ? count : (count + parts - 1) / parts;
                 width = (width + kUp - 1) & ~(kUp - 1);
-                within = (int)w;
                 left = parts * across - within;
             }
             t.g = g;
@@ -404,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     __shared__ uint64_t bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_ok;
+    __shared__ Table s_table;
     const GmmArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = kCta == 2 ? (int)cluster_rank() : 0;
@@ -425,21 +486,22 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         tc::tma_prefetch_desc(&p.tmb[0]);
         if (kDir == kGmmDw) tc::tma_prefetch_desc(&p.tmo);
     }
-    bool good = true;  // the offsets are in order, so a group's rows need no look at the groups before it
-    if (kDir == kGmmDw) good = gmm_check_offsets(a, tid, kThreads);
+    grid_wait();
+    // whether the offsets are in order, so that a group's rows need no look at the groups before it
+    bool good = true;
+    if (kDir == kGmmDw || p.table) good = gmm_check_offsets(a, tid, kThreads);
     else if (blockIdx.x == 0) (void)gmm_check_offsets(a, tid, kThreads);
     tc::tc_fence_before();
-    if (kCta == 2) {
-        __syncwarp();
-        cluster_sync();
-    } else {
-        good = __syncthreads_and(good);
-    }
+    good = __syncthreads_and(good);
+    if constexpr (kDir != kGmmDw)
+        if (p.table && good)
+            fill_table<kThreads>(s_table, a, ((kDir == kGmmFwd ? a.N : a.K) + kLanes * kCta - 1) / (kLanes * kCta), tid);
+    if (kCta == 2) cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
     Schedule<kDir, kCta> sched;
-    sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane, good);
+    sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane, good, kDir != kGmmDw && p.table && good ? &s_table : nullptr);
     const bool parts = kDir == kGmmDw && a.out_f32;  // long sums in parts
 
     if (warp == 0) {
@@ -742,19 +804,8 @@ cudaError_t launch_cta(const TcGmm& p, int64_t tiles, cudaStream_t s) {
     static SmemLimit limit;
     const cudaError_t e = limit.raise((const void*)gmm_tc_kernel<kDir, kF16, kCta>, Ring<kDir, kCta>::smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, device_sms() / kCta) * kCta);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Ring<kDir, kCta>::smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCta;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gmm_tc_kernel<kDir, kF16, kCta>, p);
+    return launch_dependent(gmm_tc_kernel<kDir, kF16, kCta>, dim3((unsigned)std::min<int64_t>(tiles, device_sms() / kCta) * kCta),
+                            kThreads, Ring<kDir, kCta>::smem, kCta, s, p);
 }
 
 template <int kDir, int kF16>
@@ -799,6 +850,7 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s
         for (int i = 0; i < 4; ++i) ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, 16 << i);
         tiles *= a.M / kCols + (a.off ? (int64_t)a.G : 1);
     }
+    p.table = dir != kGmmDw && a.off && a.G <= kTable && tiles < (1 << 30);
     if (!ok) return cudaErrorInvalidValue;
     switch (dir) {
         case kGmmFwd: return f16 ? launch_dir<kGmmFwd, 1>(p, pair, tiles, s) : launch_dir<kGmmFwd, 0>(p, pair, tiles, s);

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    grid_wait();
 #pragma unroll
     for (int i = 0; i < S::kDepth - 1; ++i) copy();  // under way while x is staged
 
@@ -377,6 +378,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
 template <int kBits>
 __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int64_t pieces, uint4* __restrict__ out) {
     const int groups8 = W.group / 8;
+    grid_release();  // the product's blocks set themselves up meanwhile
+    grid_wait();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
         uint32_t w[2];
         if (kBits == 4) {
@@ -430,8 +433,8 @@ cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
         if (cost < best) best = cost, a.split = s;
     }
     const int per = kWarps / a.split, want = (tiles + per - 1) / per;
-    linear_codes_kernel<kBits, kUnit, kNT, kMT><<<dim3(std::min(want, room), across), kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(linear_codes_kernel<kBits, kUnit, kNT, kMT>, dim3(std::min(want, room), across), kThreads, smem,
+                            1, s, a);
 }
 
 template <int kBits, int kUnit>
@@ -473,9 +476,8 @@ cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T,
 cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s) {
     const int64_t pieces = (int64_t)W.out * W.in / 8, want = (pieces + 255) / 256;
     const unsigned blocks = (unsigned)std::min<int64_t>(want, (int64_t)device_sms() * 8);
-    if (W.bits == 4) dequant16_kernel<4><<<blocks, 256, 0, s>>>(W, pieces, reinterpret_cast<uint4*>(out));
-    else dequant16_kernel<8><<<blocks, 256, 0, s>>>(W, pieces, reinterpret_cast<uint4*>(out));
-    return cudaGetLastError();
+    return launch_dependent(W.bits == 4 ? dequant16_kernel<4> : dequant16_kernel<8>, dim3(blocks), 256, 0, 1, s, W, pieces,
+                            reinterpret_cast<uint4*>(out));
 }
 
 }  // namespace moeq

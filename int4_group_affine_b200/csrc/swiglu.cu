@@ -73,6 +73,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 template <int kF16, int kGrad, int kTeam>
 __global__ void __launch_bounds__(256) swiglu_vec_kernel(const SwigluArgs a) {
     __shared__ float s_part[8];
+    grid_wait();
     const Range r = rows_of(a);
     const int I8 = a.I / 8, at = threadIdx.x % kTeam;
     for (int64_t m = r.begin + (int64_t)blockIdx.x * (256 / kTeam) + threadIdx.x / kTeam; m < r.end;
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(256) swiglu_vec_kernel(const SwigluArgs a) {
 template <int kF16, int kGrad>
 __global__ void __launch_bounds__(256) swiglu_any_kernel(const SwigluArgs a) {
     __shared__ float s_part[8];
+    grid_wait();
     const Range r = rows_of(a);
     const int64_t m = blockIdx.x;
     if (m < r.begin || m >= r.end) return;
@@ -160,13 +162,10 @@ template <int kF16, int kGrad>
 cudaError_t launch_typed(const SwigluArgs& a, cudaStream_t s) {
     const uintptr_t all = (uintptr_t)a.gu | (uintptr_t)(kGrad ? (const void*)a.dh : a.h) | (kGrad ? (uintptr_t)a.dgu : 0);
     if (a.I % 8 || (all & 15)) {
-        swiglu_any_kernel<kF16, kGrad><<<a.M, 256, 0, s>>>(a);
-    } else if (a.I >= kWide) {
-        swiglu_vec_kernel<kF16, kGrad, 256><<<a.M, 256, 0, s>>>(a);
-    } else {
-        swiglu_vec_kernel<kF16, kGrad, 32><<<(a.M + 7) / 8, 256, 0, s>>>(a);
+        return launch_dependent(swiglu_any_kernel<kF16, kGrad>, dim3(a.M), 256, 0, 1, s, a);
     }
-    return cudaGetLastError();
+    if (a.I >= kWide) return launch_dependent(swiglu_vec_kernel<kF16, kGrad, 256>, dim3(a.M), 256, 0, 1, s, a);
+    return launch_dependent(swiglu_vec_kernel<kF16, kGrad, 32>, dim3((a.M + 7) / 8), 256, 0, 1, s, a);
 }
 
 }  // namespace
