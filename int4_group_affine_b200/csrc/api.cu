@@ -918,8 +918,6 @@ moe_status moe_ep_combine(const uint16_t* ret, const int32_t* pos, const float* 
 // ------------------------------------------------- linear layers in the affine format
 namespace {
 constexpr int kMaxLinearOut = 1 << 24;
-constexpr int kLinearMatrixRows = 65;  // from this many rows on, the matrix in bf16 is multiplied
-
 // The matrix of a linear call: MOE_OK, or the status it is refused with.
 moe_status linear_check(const moe_qtensor* W) {
     if (!W || W->out <= 0 || W->in <= 0 || (W->bits != 4 && W->bits != 8)) return MOE_ERR_INVALID_ARG;
@@ -928,8 +926,18 @@ moe_status linear_check(const moe_qtensor* W) {
     return MOE_OK;
 }
 
-// Whether a forward of T rows multiplies the matrix in bf16 (else the codes).
-bool linear_matrix(const moe_qtensor* W, int T) { return T >= kLinearMatrixRows || !affine_codes_supported(*W); }
+// Whether a forward of T rows multiplies the matrix in bf16 (else the codes).  The codes are unpacked once for every 16
+// rows, the matrix once and written out, and its product goes through the inputs 64 at a time in every tile.  Fitted to
+// (us, codes | matrix) 2048 x 2048: 16 rows 5.5 | 15, 64 rows 12 | 15, 128 rows 17 | 15; 16384 outputs: 32 rows 28 | 30,
+// 64 rows 47 | 30; 1024 outputs of 8192: 64 rows 29 | 46, 192 rows 54 | 50.
+bool linear_matrix(const moe_qtensor* W, int T) {
+    if (!affine_codes_supported(*W)) return true;
+    if (T <= 16) return false;
+    const double m = (double)W->out * W->in * 1e-6;
+    const double codes = 4.0 + W->in / 1200.0 + 0.34 * m * ((T + 15) / 16);
+    const double tiles = (double)((W->out + 255) / 256) * ((T + 255) / 256), waves = ceil(tiles / 74.0);
+    return codes > 6.0 + 0.28 / 64.0 * W->in * waves + 0.45 * m;
+}
 
 // status word, then the matrix as bf16 where the call multiplies that
 size_t linear_bytes(const moe_qtensor* W, bool matrix) {

@@ -443,6 +443,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, wait_more(bar, parity, a.status, ok, a.wait_ns));
 }
 
+// The bound of a block's last waits: what is under way ends by itself, also where the waits before were cut short.
+__device__ __forceinline__ uint64_t drain_ns(const GmmArgs& a) { return a.wait_ns > 1000000000ull ? a.wait_ns : 1000000000ull; }
+
 // A place in the ring of stages, and the parity its barriers complete with next.
 template <int kStages>
 struct Place {
@@ -560,11 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 }
             }
         }
-        if (lane == 0 && !s_ok && rank == 0)
-            // given up: wait for the copies still in flight before the block ends (a pair's second block, whose
-            // copies report to the first, ends with it)
+        // No block ends with copies on their way into it, however the others fared.  (A pair's copies report to its
+        // first block; should the two have parted in giving up, the second cannot tell and lets time pass.)
+        if (one && rank == 0) {
             for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-                tc::mbar_wait(&bar_full[i % kStages], (i / kStages) & 1, a.status, a.wait_ns);
+                tc::mbar_wait(&bar_full[i % kStages], (i / kStages) & 1, a.status, drain_ns(a));
+        } else if (one && !(ok && s_ok)) {
+            for (const uint64_t t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 1000000;) {
+            }
+        }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ products
         // descriptors of stage 0; a stage, and 16 terms, are so many 16-byte units further
@@ -618,9 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 p0 = p1;
             }
         }
-        if (!ok && one) {  // given up: the products still in flight end before their memory is freed
+        if (one) {  // and none with products under way
             commit<kCta>(1, tc::smem_u32(&bar_drain));
-            tc::mbar_wait(&bar_drain, 0, a.status, a.wait_ns);
+            tc::mbar_wait(&bar_drain, 0, a.status, drain_ns(a));
         }
     } else if (warp > 1) {
         // ------------------------------------------------------------ results

@@ -372,35 +372,67 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
     }
 }
 
-// The matrix in bf16: eight codes (one 4-bit word or two 8-bit ones) to one 16-byte store a thread; bound by
-// the 2 bytes written per weight.  One rounding per weight (s q + b in fp32 is exact to its last place): the
-// tensor core multiplies 16-bit operands, and the rows it meets are rounded to as many bits.
+// The matrix in bf16, one rounding per weight (the tensor core multiplies 16-bit operands, and the rows it meets are
+// rounded to as many bits): eight codes, one 4-bit word or two 8-bit ones, to one 16-byte store, four of them a thread
+// and step so that their loads are under way together.  Bound by the 2 bytes written per weight.
+constexpr int kPieces = 4;
 template <int kBits>
-__global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int64_t pieces, uint4* __restrict__ out) {
-    const int groups8 = W.group / 8;
+__global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int64_t pieces, int shift, uint4* __restrict__ out) {
+    const int groups8 = W.group / 8;  // 1 << shift, or shift < 0
     grid_release();  // the product's blocks set themselves up meanwhile
     grid_wait();
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
-        uint32_t w[2];
-        if (kBits == 4) {
-            w[0] = __ldg(W.packed + i);
-            w[1] = w[0] >> 16;
-        } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(W.packed) + i);
-            w[0] = v.x;
-            w[1] = v.y;
-        }
-        const int64_t g = i / groups8;  // (a row is a whole number of groups)
-        const float s = bf16f(__ldg(W.scales + g)), b = bf16f(__ldg(W.biases + g));
-        uint32_t o[4];
+    for (int64_t i0 = (int64_t)blockIdx.x * (256 * kPieces) + threadIdx.x; i0 < pieces;
+         i0 += (int64_t)gridDim.x * (256 * kPieces)) {
+        uint32_t w[kPieces][kBits / 4];
+        uint16_t s[kPieces], b[kPieces];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = w[j / 2] >> (2 * kBits * (j % 2));
-            const float lo = fmaf(s, u2f_small(v & ((1u << kBits) - 1u)), b);
-            const float hi = fmaf(s, u2f_small((v >> kBits) & ((1u << kBits) - 1u)), b);
-            o[j] = (uint32_t)f2bf16(lo) | ((uint32_t)f2bf16(hi) << 16);
+        for (int j = 0; j < kPieces; ++j) {
+            const int64_t i = i0 + j * 256;
+            if (i >= pieces) break;
+            if constexpr (kBits == 4) {
+                w[j][0] = __ldg(W.packed + i);
+            } else {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(W.packed) + i);
+                w[j][0] = v.x, w[j][1] = v.y;
+            }
+            const int64_t g = shift >= 0 ? i >> shift : i / groups8;  // (a row is a whole number of groups)
+            s[j] = __ldg(W.scales + g);
+            b[j] = __ldg(W.biases + g);
         }
-        out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int64_t i = i0 + j * 256;
+            if (i >= pieces) break;
+            const __nv_bfloat162 s2 = __bfloat162bfloat162(__ushort_as_bfloat16(s[j]));
+            const __nv_bfloat162 b2 = __bfloat162bfloat162(__ushort_as_bfloat16(b[j]));
+            const __nv_bfloat162 k128 = __float2bfloat162_rn(128.0f);
+            auto nib = [&](uint32_t v) {  // the low nibbles of bytes 0 and 2 (exact)
+                const uint32_t r = nib2(v, 0);
+                return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r), k128);
+            };
+            auto affine = [&](__nv_bfloat162 q) {
+                const __nv_bfloat162 d = __hfma2(q, s2, b2);
+                return *reinterpret_cast<const uint32_t*>(&d);
+            };
+            uint32_t o[4];
+            if constexpr (kBits == 4) {  // pairs (0, 4) (1, 5) (2, 6) (3, 7)
+                uint32_t d[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) d[h] = affine(nib(w[j][0] >> (4 * h)));
+                o[0] = __byte_perm(d[0], d[1], 0x5410), o[1] = __byte_perm(d[2], d[3], 0x5410);
+                o[2] = __byte_perm(d[0], d[1], 0x7632), o[3] = __byte_perm(d[2], d[3], 0x7632);
+            } else {                     // a word: (0, 2) (1, 3); bf16 holds every whole number up to 256
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = w[j][h];
+                    const __nv_bfloat162 k16 = __float2bfloat162_rn(16.0f);
+                    const uint32_t d0 = affine(__hfma2(nib(x >> 4), k16, nib(x)));
+                    const uint32_t d1 = affine(__hfma2(nib(x >> 12), k16, nib(x >> 8)));
+                    o[2 * h] = __byte_perm(d0, d1, 0x5410), o[2 * h + 1] = __byte_perm(d0, d1, 0x7632);
+                }
+            }
+            out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
 }
 
@@ -474,9 +506,12 @@ cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T,
 }
 
 cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s) {
-    const int64_t pieces = (int64_t)W.out * W.in / 8, want = (pieces + 255) / 256;
+    const int64_t pieces = (int64_t)W.out * W.in / 8, want = (pieces + 256 * kPieces - 1) / (256 * kPieces);
     const unsigned blocks = (unsigned)std::min<int64_t>(want, (int64_t)device_sms() * 8);
-    return launch_dependent(W.bits == 4 ? dequant16_kernel<4> : dequant16_kernel<8>, dim3(blocks), 256, 0, 1, s, W, pieces,
+    int shift = 0;
+    while (8 << shift < W.group) ++shift;
+    if (8 << shift != W.group) shift = -1;
+    return launch_dependent(W.bits == 4 ? dequant16_kernel<4> : dequant16_kernel<8>, dim3(blocks), 256, 0, 1, s, W, pieces, shift,
                             reinterpret_cast<uint4*>(out));
 }
 
