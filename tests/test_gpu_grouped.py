@@ -286,3 +286,29 @@ def test_gradients_against_differences():
         tol = float((d.abs() * (up.abs() + dn.abs())).sum()) / (2 * e) * HALF["fp16"] * 1.1
         tol += float((grad.double().abs() * direction.double().abs()).sum()) * HALF["fp16"] * 1.1
         assert abs(by_diff - by_grad) <= tol, (by_diff, by_grad, tol)
+
+
+@pytest.mark.parametrize("kind", ["fwd", "dx", "dw"])
+def test_more_groups_than_a_block_tabulates(kind):
+    """2500 groups, most of them empty or of one row: (expert, adapter) pairs."""
+    g = torch.Generator().manual_seed(14)
+    sizes = (torch.randint(0, 4, (2500,), generator=g) * (torch.rand(2500, generator=g) > 0.5)).tolist()
+    sizes[1300] = 300
+    _check(kind, "bf16", sizes, 40, 48, first=2, tail=3)
+
+
+def test_on_a_given_stream():
+    """The stream argument: work follows what that stream did before."""
+    m = _m()
+    sizes, N, K = [50, 0, 70], 128, 256
+    x, dy, W, off, M = _case(15, sizes, N, K, "bf16")
+    s = torch.cuda.Stream()
+    xs = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2000000)
+        xs.copy_(x)
+    out, st = _run("fwd", "bf16", xs, dy, W, off, M, 3, N, K, stream=s)
+    ref, mag, n = grouped_ref("fwd", off, x, W, dy)
+    assert st == 0
+    assert_within(out, ref, HALF["bf16"] * ref.abs() + 1.01 * sum_err(n, mag))
