@@ -1,13 +1,19 @@
 // grouped.cu - products grouped by expert with ragged sizes, and their gradients, on warp-level
-// tensor-core tiles: the kernel that takes every size, alignment and row count.
+// tensor-core tiles: the kernel that takes every size and alignment.  Operands whose rows are whole
+// 16-byte pieces go to the tcgen05 kernel (grouped_tc.cu) instead; TMA cannot read others.
 //
-// A block owns a 64 x 64 tile of the output and steps through the sum 32 terms at a time: both
-// operands come into shared memory by guarded 2-byte loads (zero outside the matrix and, for the
-// weight gradient, outside the group's rows, so a NaN in another group's row never meets a sum),
-// laid out [row][term] with an 80-byte pitch (the eight rows a fragment load touches start 20 banks
-// apart: no two of its 32 words share a bank), and four warps of 32 x 32 run mma.sync m16n8k16 with
-// fp32 accumulators.  The loads follow the operand's contiguous axis, so they coalesce in all three
-// directions.
+// A block owns a 128 x 128 tile of the output and steps through the sum 32 terms at a time.  Rows may
+// start at any element, so the aligned 16-byte pieces that they lie in are copied as they are
+// (cp.async, four steps ahead: the copies' latency is what a block with few tiles beside it waits
+// for), and on their way from there to the tile the elements are shifted into place (a row's shift
+// is the same in every step, which advances by 64 bytes or by 32 whole rows) and whatever lies outside
+// the matrix or, for the weight gradient, outside the group's rows becomes zero, so a NaN in another
+// group's row never meets a sum.  No byte outside the tensors is read.  Eight warps of 64 x 32 run
+// mma.sync m16n8k16 (fp32 accumulators) on the tile.  An operand whose terms are contiguous in memory
+// is kept [row][term], one whose rows are, [term][row], which ldmatrix transposes; pitches of 80 and
+// 272 bytes put the eight rows of an ldmatrix in different banks.
+//
+// Bound by the warp-level tensor path (about a quarter of tcgen05's rate) and its feeding.
 #include <cuda_fp16.h>
 
 #include "grouped.cuh"
@@ -15,26 +21,41 @@
 namespace moeq {
 namespace {
 
-constexpr int kT = 64, kKT = 32, kPitch = 40, kThreads = 128;
-// fp32 results: the tensor core's fp32 accumulation rounds toward zero, an error that grows with
-// the length of the sum (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192); sums longer
-// than this are added up in parts of this length with rounded fp32 additions.
+constexpr int kT = 128, kKT = 32, kThreads = 256, kAhead = 4;
+constexpr int kPitchT = kKT + 8;  // [row][term]
+constexpr int kPitchR = kT + 8;   // [term][row]
+// fp32 results: the tensor core's fp32 accumulation rounds toward zero, an error that grows with the length of the
+// sum (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192); longer sums are added up in parts of this length
+// with rounded fp32 additions.
 constexpr int kPart = 512;
 
 template <int kF16>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (kF16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
             "%2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
             "%1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int kTrans>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const uint16_t* p) {
+    const uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
+    if (kTrans)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
 }
 
 template <int kF16>
@@ -46,27 +67,134 @@ __device__ __forceinline__ float from16(uint16_t v) {
     return kF16 ? __half2float(__ushort_as_half(v)) : bf16f(v);
 }
 
-// One operand tile [64 rows][32 terms] into shared memory.  kAlong: 0 the terms are contiguous in
-// memory (row stride ld), 1 the rows are (term stride ld).
-template <int kAlong>
-__device__ __forceinline__ void load_tile(uint16_t (*s)[kPitch], const uint16_t* __restrict__ p, int64_t ld, int r0,
-                                          int rows, int t0, int terms, int tid) {
-    if (kAlong == 0) {
-        const int t = tid % kKT;
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // (the rest of the 16: zeros)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Eight 16-bit elements out of the two aligned pieces they lie in, from byte `off` on; the first n count.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, int off, int n) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (off & 8) {
 #pragma unroll
-        for (int r = tid / kKT; r < kT; r += kThreads / kKT)
-            s[r][t] = (r0 + r < rows && t0 + t < terms) ? __ldg(p + (int64_t)(r0 + r) * ld + t0 + t) : (uint16_t)0;
-    } else {
-        const int r = tid % kT;
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
 #pragma unroll
-        for (int t = tid / kT; t < kKT; t += kThreads / kT)
-            s[r][t] = (r0 + r < rows && t0 + t < terms) ? __ldg(p + (int64_t)(t0 + t) * ld + r0 + r) : (uint16_t)0;
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (off & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    if (n < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (2 * i + 1 >= n) w[i] &= 0xFFFFu;
+            if (2 * i >= n) w[i] = 0;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A piece that may reach outside the tensor [first, last).
+__device__ __noinline__ void copy_edge(unsigned char* dst, const char* src, const uint16_t* first, const uint16_t* last) {
+    const char *begin = reinterpret_cast<const char*>(first), *end = reinterpret_cast<const char*>(last);
+    if (src >= begin) {
+        const int bytes = (int)min((int64_t)16, max((int64_t)0, (int64_t)(end - src)));
+        cp16((uint32_t)__cvta_generic_to_shared(dst), bytes ? src : begin, bytes);
+    } else {  // the tensor begins inside the piece
+        for (int b = (int)(begin - src); b < 16 && src + b < end; b += 2)
+            *reinterpret_cast<uint16_t*>(dst + b) = __ldg(reinterpret_cast<const uint16_t*>(src + b));
     }
 }
 
-template <int kDir, int kF16>
-__global__ void __launch_bounds__(kThreads) gmm_any_kernel(const GmmArgs a) {
-    __shared__ __align__(16) uint16_t sA[kT][kPitch], sB[kT][kPitch];
+// One operand of the tile: 128 rows x 32 terms a step.  kRows: the rows are contiguous in memory (else the terms).  A
+// line is what is contiguous of a step: a row's 32 terms, or a term's 128 rows.
+template <int kRows>
+struct Operand {
+    static constexpr int kElems = kRows ? kKT * kPitchR : kT * kPitchT;
+    static constexpr int kLines = kRows ? kKT : kT, kEights = kRows ? kT / 8 : kKT / 8;
+    static constexpr int kPieces = kEights + 1;              // aligned pieces a line lies in
+    static constexpr int kRaw = kLines * kPieces * 16;       // bytes of a step
+    const uint16_t *p, *first, *last;  // the group's first element; the tensor
+    int64_t ld;
+    int row0, rows, terms;
+
+    __device__ __forceinline__ const uint16_t* line(int t0, int i) const {
+        return kRows ? p + (int64_t)(t0 + i) * ld + row0 : p + (int64_t)(row0 + i) * ld + t0;
+    }
+    __device__ __forceinline__ bool live(int t0, int i) const { return kRows ? t0 + i < terms : row0 + i < rows; }
+
+    // What stays the same from step to step, for this thread's pieces and eights: where they are, and whether a whole
+    // step's are all inside the tensor.
+    static constexpr int kCopies = (kLines * kPieces + kThreads - 1) / kThreads, kPlaces = kLines * kEights / kThreads;
+    const char* src[kCopies];
+    bool safe[kCopies];
+    int off[kPlaces], count[kPlaces];
+
+    __device__ __forceinline__ void start(int tid) {
+        const int64_t steps = terms / kKT;  // whole ones
+#pragma unroll
+        for (int h = 0; h < kCopies; ++h) {
+            const int i = tid + h * kThreads, l = min(i / kPieces, kLines - 1);
+            src[h] = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(line(0, l)) & ~(uintptr_t)15) + i % kPieces * 16;
+            safe[h] = i < kLines * kPieces && steps > 0 && (kRows || live(0, l)) &&
+                      src[h] >= reinterpret_cast<const char*>(first) &&
+                      src[h] + (steps - 1) * (kRows ? ld * (2 * kKT) : 2 * kKT) + 16 <= reinterpret_cast<const char*>(last);
+        }
+#pragma unroll
+        for (int h = 0; h < kPlaces; ++h) {
+            const int i = tid + h * kThreads, l = i / kEights;
+            off[h] = (int)(reinterpret_cast<uintptr_t>(line(0, l)) & 15);
+            count[h] = kRows ? min(max(rows - (row0 + i % kEights * 8), 0), 8) : live(0, l) ? 8 : 0;
+        }
+    }
+    __device__ __forceinline__ void copy(unsigned char* raw, int t0, int tid) {
+        const bool whole = t0 + kKT <= terms;
+        const uint32_t dst0 = (uint32_t)__cvta_generic_to_shared(raw) + tid * 16;
+#pragma unroll
+        for (int h = 0; h < kCopies; ++h) {
+            if (whole && safe[h]) cp16(dst0 + h * kThreads * 16, src[h], 16);
+            else if (tid + h * kThreads < kLines * kPieces && live(t0, (tid + h * kThreads) / kPieces))
+                copy_edge(raw + (tid + h * kThreads) * 16, src[h], first, last);
+            src[h] += kRows ? ld * (2 * kKT) : 2 * kKT;  // (32 rows are whole pieces whatever their length)
+        }
+    }
+    __device__ __forceinline__ void place(uint16_t* s, const unsigned char* raw, int t0, int tid) const {
+        const bool whole = t0 + kKT <= terms;
+#pragma unroll
+        for (int h = 0; h < kPlaces; ++h) {
+            const int i = tid + h * kThreads, l = i / kEights, c = i % kEights;
+            int n = count[h];
+            if (!whole) n = kRows ? (live(t0, l) ? n : 0) : min(n, max(terms - (t0 + c * 8), 0));
+            const uint4* at = reinterpret_cast<const uint4*>(raw) + l * kPieces + c;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (n > 0) v = shifted(at[0], at[1], off[h], n);
+            *reinterpret_cast<uint4*>(s + l * (kRows ? kPitchR : kPitchT) + c * 8) = v;
+        }
+    }
+    // mma.sync's A fragment of rows [r, r + 16), terms [k, k + 16)
+    __device__ __forceinline__ static void frag_a(uint32_t (&f)[4], const uint16_t* s, int r, int k, int lane) {
+        const int q = lane / 8, l = lane % 8;
+        if (kRows) ldmatrix4<1>(f, s + (k + q / 2 * 8 + l) * kPitchR + r + q % 2 * 8);
+        else ldmatrix4<0>(f, s + (r + q % 2 * 8 + l) * kPitchT + k + q / 2 * 8);
+    }
+    // and two B fragments (b0, b1 of rows [r, r + 8), then of [r + 8, r + 16))
+    __device__ __forceinline__ static void frag_b(uint32_t (&f)[4], const uint16_t* s, int r, int k, int lane) {
+        const int q = lane / 8, l = lane % 8;
+        if (kRows) ldmatrix4<1>(f, s + (k + q % 2 * 8 + l) * kPitchR + r + q / 2 * 8);
+        else ldmatrix4<0>(f, s + (r + q / 2 * 8 + l) * kPitchT + k + q % 2 * 8);
+    }
+};
+
+// kParts: fp32 weight gradients (sums in parts).
+template <int kDir, int kF16, int kParts>
+__global__ void __launch_bounds__(kThreads, kParts ? 1 : 2) gmm_any_kernel(const GmmArgs a) {
+    using A = Operand<kDir == kGmmDw>;
+    using B = Operand<kDir != kGmmFwd>;
+    extern __shared__ __align__(16) unsigned char sm[];  // [steps ahead][A, B], then the tile
+    constexpr int kRaw = A::kRaw + B::kRaw;
+    uint16_t *sA = reinterpret_cast<uint16_t*>(sm + kAhead * kRaw), *sB = sA + A::kElems;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g8 = lane / 4, c4 = lane % 4;
     grid_wait();
     if (blockIdx.x == 0) (void)gmm_check_offsets(a, tid, kThreads);
@@ -96,51 +224,78 @@ __global__ void __launch_bounds__(kThreads) gmm_any_kernel(const GmmArgs a) {
         S = kDir == kGmmFwd ? a.K : a.N;
     }
     const int64_t nk = (int64_t)a.N * a.K;
-    const uint16_t* pa = kDir == kGmmDw ? a.a + (int64_t)rows.begin * a.N : a.a + (int64_t)rows.begin * S;
-    const uint16_t* pb = kDir == kGmmDw ? a.b + (int64_t)rows.begin * a.K : a.b + g * nk;
+    const int la = kDir == kGmmFwd ? a.K : a.N;  // a row of the first operand
+    A oa;
+    oa.first = a.a;
+    oa.last = a.a + (int64_t)a.M * la;
+    oa.p = a.a + (int64_t)rows.begin * la;
+    oa.ld = la;
+    oa.row0 = i0;
+    oa.rows = I;
+    oa.terms = S;
+    B ob;
+    ob.first = a.b;
+    ob.last = a.b + (kDir == kGmmDw ? (int64_t)a.M * a.K : a.G * nk);
+    ob.p = kDir == kGmmDw ? a.b + (int64_t)rows.begin * a.K : a.b + g * nk;
+    ob.ld = a.K;
+    ob.row0 = j0;
+    ob.rows = J;
+    ob.terms = S;
 
-    float acc[2][4][4], sum[2][4][4];
+    float acc[4][4][4], sum[kParts ? 4 : 1][4][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][j][q] = sum[i][j][q] = 0.0f;
+            for (int q = 0; q < 4; ++q) {
+                acc[i][j][q] = 0.0f;
+                if (kParts) sum[kParts ? i : 0][j][q] = 0.0f;
+            }
 
-    const int wi = warp / 2 * 32, wj = warp % 2 * 32;
+    const int wi = warp / 4 * 64, wj = warp % 4 * 32;
+    oa.start(tid);
+    ob.start(tid);
+    auto copy = [&](int t0) {
+        if (t0 < S) {
+            unsigned char* raw = sm + t0 / kKT % kAhead * kRaw;
+            oa.copy(raw, t0, tid);
+            ob.copy(raw + A::kRaw, t0, tid);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int h = 0; h < kAhead - 1; ++h) copy(h * kKT);
     for (int t0 = 0; t0 < S; t0 += kKT) {
-        __syncthreads();
-        load_tile<kDir == kGmmDw>(sA, pa, kDir == kGmmDw ? a.N : S, i0, I, t0, S, tid);
-        load_tile<kDir != kGmmFwd>(sB, pb, a.K, j0, J, t0, S, tid);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+        __syncthreads();  // the step's pieces are there, and the tile and the step before's pieces are read
+        copy(t0 + (kAhead - 1) * kKT);
+        const unsigned char* raw = sm + t0 / kKT % kAhead * kRaw;
+        oa.place(sA, raw, t0, tid);
+        ob.place(sB, raw + A::kRaw, t0, tid);
         __syncthreads();
 #pragma unroll
         for (int ks = 0; ks < kKT; ks += 16) {
-            uint32_t fa[2][4];
+            uint32_t fb[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = wi + 16 * i + g8, k = ks + 2 * c4;
-                fa[i][0] = *reinterpret_cast<const uint32_t*>(&sA[r][k]);
-                fa[i][1] = *reinterpret_cast<const uint32_t*>(&sA[r + 8][k]);
-                fa[i][2] = *reinterpret_cast<const uint32_t*>(&sA[r][k + 8]);
-                fa[i][3] = *reinterpret_cast<const uint32_t*>(&sA[r + 8][k + 8]);
-            }
+            for (int j = 0; j < 2; ++j) B::frag_b(fb[j], sB, wj + 16 * j, ks, lane);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = wj + 8 * j + g8, k = ks + 2 * c4;
-                const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&sB[r][k]);
-                const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&sB[r][k + 8]);
-                mma16<kF16>(acc[0][j], fa[0], b0, b1);
-                mma16<kF16>(acc[1][j], fa[1], b0, b1);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t fa[4];
+                A::frag_a(fa, sA, wi + 16 * i, ks, lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma16<kF16>(acc[i][j], fa, fb[j / 2][j % 2 * 2], fb[j / 2][j % 2 * 2 + 1]);
             }
         }
-        if ((t0 + kKT) % kPart == 0 || t0 + kKT >= S) {
+        if (kParts && ((t0 + kKT) % kPart == 0 || t0 + kKT >= S)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        sum[i][j][q] += acc[i][j][q];
+                        sum[kParts ? i : 0][j][q] += acc[i][j][q];
                         acc[i][j][q] = 0.0f;
                     }
         }
@@ -148,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) gmm_any_kernel(const GmmArgs a) {
 
     const int64_t out0 = kDir == kGmmDw ? g * nk : (int64_t)rows.begin * J;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -156,27 +311,41 @@ __global__ void __launch_bounds__(kThreads) gmm_any_kernel(const GmmArgs a) {
                 const int r = i0 + wi + 16 * i + g8 + 8 * (q / 2), c = j0 + wj + 8 * j + 2 * c4 + q % 2;
                 if (r >= I || c >= J) continue;
                 const int64_t at = out0 + (int64_t)r * J + c;
-                float v = sum[i][j][q];
-                if (kDir == kGmmDw && a.out_f32) {
+                if (kParts) {
                     float* o = reinterpret_cast<float*>(a.out) + at;
+                    const float v = sum[kParts ? i : 0][j][q];
                     *o = a.accumulate ? *o + v : v;
                 } else {
                     uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+                    float v = acc[i][j][q];
                     if (kDir == kGmmDw && a.accumulate) v += from16<kF16>(*o);
                     *o = to16<kF16>(v);
                 }
             }
 }
 
-template <int kDir>
-cudaError_t launch_any(const GmmArgs& a, int f16, cudaStream_t s) {
+template <int kDir, int kF16, int kParts>
+cudaError_t launch_parts(const GmmArgs& a, unsigned tiles, cudaStream_t s) {
+    using A = Operand<kDir == kGmmDw>;
+    using B = Operand<kDir != kGmmFwd>;
+    constexpr size_t smem = kAhead * (A::kRaw + B::kRaw) + (A::kElems + B::kElems) * 2;
+    static_assert(2 * smem <= 227 * 1024 - 2048, "two blocks a multiprocessor");
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise((const void*)gmm_any_kernel<kDir, kF16, kParts>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(gmm_any_kernel<kDir, kF16, kParts>, dim3(tiles), kThreads, smem, 1, s, a);
+}
+
+template <int kDir, int kF16>
+cudaError_t launch_any(const GmmArgs& a, cudaStream_t s) {
     const int64_t jt = ((kDir == kGmmFwd ? a.N : a.K) + kT - 1) / kT;
     // forward and dx: a group's last tile may be partly filled, so at most one more per group
     const int64_t tiles = kDir == kGmmDw ? (int64_t)a.G * ((a.N + kT - 1) / kT) * jt
                                          : ((int64_t)a.M / kT + (a.off ? a.G : 1)) * jt;
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch_dependent(f16 ? gmm_any_kernel<kDir, 1> : gmm_any_kernel<kDir, 0>, dim3((unsigned)tiles), kThreads, 0, 1, s,
-                            a);
+    if constexpr (kDir == kGmmDw)
+        if (a.out_f32) return launch_parts<kDir, kF16, 1>(a, (unsigned)tiles, s);
+    return launch_parts<kDir, kF16, 0>(a, (unsigned)tiles, s);
 }
 
 }  // namespace
@@ -184,9 +353,9 @@ cudaError_t launch_any(const GmmArgs& a, int f16, cudaStream_t s) {
 cudaError_t launch_grouped(int dir, int f16, const GmmArgs& a, cudaStream_t s) {
     if (grouped_tc_supported(dir, a)) return launch_grouped_tc(dir, f16, a, s);
     switch (dir) {
-        case kGmmFwd: return launch_any<kGmmFwd>(a, f16, s);
-        case kGmmDx: return launch_any<kGmmDx>(a, f16, s);
-        default: return launch_any<kGmmDw>(a, f16, s);
+        case kGmmFwd: return f16 ? launch_any<kGmmFwd, 1>(a, s) : launch_any<kGmmFwd, 0>(a, s);
+        case kGmmDx: return f16 ? launch_any<kGmmDx, 1>(a, s) : launch_any<kGmmDx, 0>(a, s);
+        default: return f16 ? launch_any<kGmmDw, 1>(a, s) : launch_any<kGmmDw, 0>(a, s);
     }
 }
 
