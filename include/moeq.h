@@ -469,8 +469,8 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  *    the frozen packed weights (adapter training over the int4 base, section 二 of that page).
  * W: one matrix (n = 1) of either affine format, any `out`, group a multiple of 32 that divides
  * `in`, packed words 16-byte aligned; out, in <= MOEQ_MAX_WIDTH or MOE_ERR_UNSUPPORTED (out: up to
- * 1 << 24).  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out]; outputs may
- * not alias inputs.  fp32 accumulation.  With few rows (16, or a few times as many for
+ * 1 << 24).  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
+ * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  With few rows (16, or a few times as many for
  * small matrices) the codes enter the sums as whole numbers, s and b once per group; larger T, and every
  * dx, first writes the matrix into the workspace as bf16 (one rounding per weight, at most 2^-8 of it)
  * and multiplies that.  An infinite

@@ -918,6 +918,7 @@ moe_status moe_ep_combine(const uint16_t* ret, const int32_t* pos, const float* 
 // ------------------------------------------------- linear layers in the affine format
 namespace {
 constexpr int kMaxLinearOut = 1 << 24;
+
 // The matrix of a linear call: MOE_OK, or the status it is refused with.
 moe_status linear_check(const moe_qtensor* W) {
     if (!W || W->out <= 0 || W->in <= 0 || (W->bits != 4 && W->bits != 8)) return MOE_ERR_INVALID_ARG;
@@ -926,44 +927,86 @@ moe_status linear_check(const moe_qtensor* W) {
     return MOE_OK;
 }
 
+// How a linear call that multiplies the matrix in bf16 is laid out: the sums of a product with few tiles are split over
+// the blocks that would be idle (at least four steps of 64 terms each).
+struct LinearPlan {
+    int splits, per, pitch;           // parts, their terms, and the pitch of the rows read
+    size_t matrix, rows, parts, total;  // workspace offsets and size
+};
+LinearPlan linear_plan(const moe_qtensor* W, int T, bool dx) {
+    LinearPlan p;
+    const int64_t J = dx ? W->in : W->out, terms = dx ? W->out : W->in, steps = (terms + 63) / 64;
+    int at_once = 1;
+    const int64_t tiles = grouped_tc_tiles(std::max(T, 1), J, &at_once);
+    const int64_t want = std::max<int64_t>(1, std::min(at_once / tiles, steps / 4));
+    p.per = (int)((steps + want - 1) / want * 64);
+    p.splits = (int)((terms + p.per - 1) / p.per);
+    p.pitch = (int)((terms + 7) / 8 * 8);
+    p.matrix = kAlign;  // behind the status word
+    p.rows = p.matrix + align_up((size_t)W->out * W->in * 2);
+    p.parts = p.rows + (p.pitch != terms ? align_up((size_t)T * p.pitch * 2) : 0);
+    // The parts, as much as any number of rows up to T takes (a workspace for some rows serves fewer too): rows in c
+    // blocks of 256 are split at most min(at_once / (lane blocks * c), steps / 4) times.
+    const int64_t blocks = (std::max(T, 1) + 255) / 256, lanes = tiles / blocks;
+    int64_t rows = 0;
+    for (int64_t c = 1; c <= blocks; ++c) {
+        const int64_t most = std::min<int64_t>(at_once / (lanes * c), steps / 4);
+        if (most < 2) break;
+        rows = std::max(rows, most * std::min<int64_t>(T, 256 * c));
+    }
+    p.total = p.parts + align_up((size_t)rows * J * 4);
+    return p;
+}
+
 // Whether a forward of T rows multiplies the matrix in bf16 (else the codes).  The codes are unpacked once for every 16
 // rows, the matrix once and written out, and its product goes through the inputs 64 at a time in every tile.  Fitted to
-// (us, codes | matrix) 2048 x 2048: 16 rows 5.5 | 15, 64 rows 12 | 15, 128 rows 17 | 15; 16384 outputs: 32 rows 28 | 30,
-// 64 rows 47 | 30; 1024 outputs of 8192: 64 rows 29 | 46, 192 rows 54 | 50.
+// (us, codes | matrix) 2048 x 2048: 16 rows 5.5 | 12, 64 rows 12 | 12, 128 rows 17 | 12; 16384 outputs of 2048: 32 rows
+// 28 | 32, 64 rows 47 | 32; 1024 outputs of 8192: 17 rows 17 | 15, 64 rows 29 | 15, 192 rows 53 | 17.
 bool linear_matrix(const moe_qtensor* W, int T) {
     if (!affine_codes_supported(*W)) return true;
     if (T <= 16) return false;
     const double m = (double)W->out * W->in * 1e-6;
     const double codes = 4.0 + W->in / 1200.0 + 0.34 * m * ((T + 15) / 16);
     const double tiles = (double)((W->out + 255) / 256) * ((T + 255) / 256), waves = ceil(tiles / 74.0);
-    return codes > 6.0 + 0.28 / 64.0 * W->in * waves + 0.45 * m;
+    const LinearPlan p = linear_plan(W, T, false);
+    return codes > (p.splits > 1 ? 9.5 : 6.0) + 0.28 / 64.0 * p.per * waves + 0.45 * m;
 }
 
-// status word, then the matrix as bf16 where the call multiplies that
-size_t linear_bytes(const moe_qtensor* W, bool matrix) {
-    return kAlign + (matrix ? align_up((size_t)W->out * W->in * 2) : 0);
-}
-
-// One group of T rows on the matrix in the workspace.
-GmmArgs linear_gmm(const moe_qtensor* W, const uint16_t* rows, int T, uint16_t* out, void* ws) {
+// The matrix as bf16, then rows times it: y [T][out] of x [T][in], or dx [T][in] of dy [T][out].
+moe_status linear_product(const moe_qtensor* W, bool dx, const uint16_t* rows, int T, uint16_t* out, void* ws,
+                          cudaStream_t s) {
+    const LinearPlan p = linear_plan(W, T, dx);
+    char* b = (char*)ws;
+    LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)(b + p.matrix), s));
+    const int terms = dx ? W->out : W->in;
+    if (p.pitch != terms) {
+        LAUNCH(kPadRows, launch_pad_rows(rows, T, terms, (uint16_t*)(b + p.rows), s));
+        rows = (const uint16_t*)(b + p.rows);
+    }
     GmmArgs a;
     memset(&a, 0, sizeof(a));
     a.a = rows;
-    a.b = (const uint16_t*)((char*)ws + kAlign);
+    a.b = (const uint16_t*)(b + p.matrix);
     a.out = out;
     a.M = T;
     a.G = 1;
     a.N = W->out;
     a.K = W->in;
+    a.splits = p.splits;
+    a.per = p.per;
+    a.partial = (float*)(b + p.parts);
     a.status = (int32_t*)ws;
     a.wait_ns = wait_limit_ns();
-    return a;
+    LAUNCH(dx ? kGroupedDx : kGroupedFwd, launch_grouped_tc(dx ? kGmmDx : kGmmFwd, 0, a, p.pitch, s));
+    if (p.splits > 1)
+        LAUNCH(kAddParts, launch_add_parts(a.partial, p.splits, (int64_t)T * (dx ? W->in : W->out), out, s));
+    return MOE_OK;
 }
 }  // namespace
 
 size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T) {
     if (T < 0 || linear_check(W) != MOE_OK) return 0;
-    return linear_bytes(W, linear_matrix(W, T));
+    return T > 0 && linear_matrix(W, T) ? linear_plan(W, T, false).total : kAlign;
 }
 
 moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y, void* workspace,
@@ -977,18 +1020,14 @@ moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T,
     CHECK_ARG(x && y && x != y && aligned(x, 16) && aligned(y, 2));
     cudaStream_t s = (cudaStream_t)stream;
     timing_begin(s);
-    if (linear_matrix(W, T)) {
-        LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)((char*)workspace + kAlign), s));
-        LAUNCH(kGroupedFwd, launch_grouped(kGmmFwd, 0, linear_gmm(W, x, T, y, workspace), s));
-        return MOE_OK;
-    }
+    if (linear_matrix(W, T)) return linear_product(W, false, x, T, y, workspace, s);
     LAUNCH(kAffineLinear, launch_affine_linear(*W, x, T, y, s));
     return MOE_OK;
 }
 
 size_t moe_affine_linear_dx_workspace_bytes(const moe_qtensor* W, int32_t T) {
     if (T < 0 || linear_check(W) != MOE_OK) return 0;
-    return linear_bytes(W, true);
+    return T > 0 ? linear_plan(W, T, true).total : kAlign;
 }
 
 moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* dy, int32_t T, uint16_t* dx, void* workspace,
@@ -996,15 +1035,13 @@ moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* dy, int32_
     moe_status st = linear_check(W);
     if (st != MOE_OK) return st;
     CHECK_ARG(T >= 0);
-    st = ws_check(workspace, ws_bytes, linear_bytes(W, true));
+    st = ws_check(workspace, ws_bytes, moe_affine_linear_dx_workspace_bytes(W, T));
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
-    CHECK_ARG(dy && dx && dy != dx && aligned(dx, 16) && aligned(dy, 2));
+    CHECK_ARG(dy && dx && dy != dx && aligned(dx, 16) && aligned(dy, W->out % 8 ? 2 : 16));
     cudaStream_t s = (cudaStream_t)stream;
     timing_begin(s);
-    LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)((char*)workspace + kAlign), s));
-    LAUNCH(kGroupedDx, launch_grouped(kGmmDx, 0, linear_gmm(W, dy, T, dx, workspace), s));
-    return MOE_OK;
+    return linear_product(W, true, dy, T, dx, workspace, s);
 }
 
 // ------------------------------------------------------- products grouped by expert

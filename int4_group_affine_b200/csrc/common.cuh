@@ -197,7 +197,7 @@ enum Kind {
     kPack, kDequant, kRouter, kTopk, kIndexCount, kIndexScan, kIndexScatter, kLoraA, kGateUp, kDown,
     kCombine, kRmsnorm, kMixedGateUp, kMixedDown, kMixedLinear, kDecode, kTcLoraGUKind, kTcGUKind,
     kTcLoraDownKind, kTcDownKind, kTcRouterKind, kKpermKind, kDecodeChain, kPrerouter, kAct8, kMixedA8, kEpDispatch, kEpCombine, kDecodeCluster,
-    kAffineLinear, kAffineDequant, kGroupedFwd, kGroupedDx, kGroupedDw, kSwiglu, kSwigluGrad, kKindCount
+    kAffineLinear, kAffineDequant, kPadRows, kAddParts, kGroupedFwd, kGroupedDx, kGroupedDw, kSwiglu, kSwigluGrad, kKindCount
 };
 void timing_begin(cudaStream_t s);
 void timing_mark(int kind, cudaStream_t s);
@@ -321,6 +321,9 @@ cudaError_t launch_ep_combine(const uint16_t* ret, const int32_t* pos, const flo
 bool affine_codes_supported(const moe_qtensor& W);
 cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T, uint16_t* y, cudaStream_t s);
 cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s);
+// Rows copied to a pitch of whole 16-byte pieces; fp32 parts [splits][n] added up to bf16 [n].
+cudaError_t launch_pad_rows(const uint16_t* x, int T, int n, uint16_t* out, cudaStream_t s);
+cudaError_t launch_add_parts(const float* parts, int splits, int64_t n, uint16_t* y, cudaStream_t s);
 
 // Products grouped by expert (csrc/grouped.cu; arguments in grouped.cuh).
 struct GmmArgs;

@@ -351,7 +351,7 @@ cudaError_t launch_any(const GmmArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_grouped(int dir, int f16, const GmmArgs& a, cudaStream_t s) {
-    if (grouped_tc_supported(dir, a)) return launch_grouped_tc(dir, f16, a, s);
+    if (grouped_tc_supported(dir, a)) return launch_grouped_tc(dir, f16, a, 0, s);
     switch (dir) {
         case kGmmFwd: return f16 ? launch_any<kGmmFwd, 1>(a, s) : launch_any<kGmmFwd, 0>(a, s);
         case kGmmDx: return f16 ? launch_any<kGmmDx, 1>(a, s) : launch_any<kGmmDx, 0>(a, s);

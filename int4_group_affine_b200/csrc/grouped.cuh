@@ -20,13 +20,20 @@ struct GmmArgs {
     int M, G, N, K;
     int out_f32;         // dw: fp32 output instead of the inputs' type
     int accumulate;      // dw: out += instead of out =
+    // forward and dx of one group without offsets: the sum in `splits` parts of `per` terms (a multiple of 64), each
+    // written as fp32 [splits][M][outputs] to `partial` instead of `out`; splits <= 1: not split
+    int splits, per;
+    float* partial;
     int32_t* status;
     uint64_t wait_ns;
 };
 
 // The tcgen05 kernel (grouped_tc.cu), and whether it takes these operands.
 bool grouped_tc_supported(int dir, const GmmArgs& a);
-cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s);
+// `pitch`: elements from one row of a.a to the next (0: as many as the sum has terms).
+cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cudaStream_t s);
+// Tiles of one group of M rows by J outputs there, and how many run at once.
+int64_t grouped_tc_tiles(int64_t M, int64_t J, int* at_once);
 
 // A group's rows.  The device sees the offsets for the first time, so whatever they hold no row
 // may be touched out of range or by two groups: they are clamped to [0, M] and a running maximum

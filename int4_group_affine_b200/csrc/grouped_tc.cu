@@ -77,7 +77,9 @@ struct Tile {
     int col0;      // first column: row of x / dy (forward, dx), input k (dw)
     int cols;      // columns that count
     int width;     // columns multiplied: cols rounded up
-    int terms;     // length of the sum
+    int terms;     // the sum runs to this term
+    int first;     // from this one on (0 but where the sum is split)
+    int part;      // and is this part of it
     int row0;      // dw: first row of the group
 };
 
@@ -160,7 +162,8 @@ struct Schedule {
     int within, step, step_g;              // dw: tile within the group, and the stride in groups and tiles
     int parts, width;                      // forward, dx: tiles along the group's rows, and their width
     int64_t tile;
-    float inv;
+    int real;                              // forward, dx: lane blocks of a part of the sum
+    float inv, inv_real;
 
     __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane, bool good_, const Table* table_) {
         good = good_;
@@ -174,7 +177,9 @@ struct Schedule {
             step = (int)(stride % left);
             fetch(a, lane);
         } else {
-            across = ((kDir == kGmmFwd ? a.N : a.K) + kTileLanes - 1) / kTileLanes;
+            real = ((kDir == kGmmFwd ? a.N : a.K) + kTileLanes - 1) / kTileLanes;
+            inv_real = 1.0f / (float)real;
+            across = real * max(a.splits, 1);
             tile = first;
             step = (int)stride;
             left = 0;
@@ -201,6 +206,7 @@ struct Schedule {
             t.cols = min(kCols, a.K - t.col0);
             t.width = (t.cols + kUp - 1) & ~(kUp - 1);
             t.terms = rows.end - rows.begin;
+            t.first = t.part = 0;
             t.row0 = rows.begin;
             within += step;
             int ng = g + step_g;
@@ -228,10 +234,17 @@ struct Schedule {
             }
             t.g = g;
             const Quot p = quot(within, across, inv);
-            t.lane0 = p.r * kTileLanes;
+            const Quot l = a.splits > 1 ? quot(p.r, real, inv_real) : Quot{0, p.r};
+            t.part = l.q;
+            t.lane0 = l.r * kTileLanes;
             t.col0 = rows.begin + p.q * width;
             t.cols = min(width, rows.end - t.col0);
             t.terms = kDir == kGmmFwd ? a.K : a.N;
+            t.first = 0;
+            if (a.splits > 1) {
+                t.first = t.part * a.per;
+                t.terms = min(t.terms, t.first + a.per);
+            }
             t.width = (t.cols + kUp - 1) & ~(kUp - 1);
             within += step;
             left -= step;
@@ -520,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             const int lanes = t.lane0 + kLanes * rank, half = t.width / kCta, col = t.col0 + half * rank;
             const int bk = (half + 63) / 64;  // dw: boxes of 64 columns
             const uint32_t bytes = kABytes + (kDir == kGmmDw ? (p.wide_b ? kCols / 64 : bk) * kBox : half * 128);
-            for (int k = 0; k < t.terms; k += kStep, at.next(), ++n) {
+            for (int k = t.first; k < t.terms; k += kStep, at.next(), ++n) {
                 ok = warp_wait(&bar_empty[at.st], at.phase ^ 1, a, &s_ok);  // (free from the start)
                 if (!ok) break;
                 const uint32_t sa = sbase + at.st * kStageBytes, sb = sa + kABytes, full = full0 + 8 * at.st;
@@ -587,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
             const uint32_t idesc = idesc_of<kDir, kCta>(kF16, t.width);
-            for (int p0 = 0; ok && p0 < t.terms; ++acc) {
+            for (int p0 = t.first; ok && p0 < t.terms; ++acc) {
                 const int p1 = parts ? min(t.terms, p0 + kPart) : t.terms;
                 const uint32_t d = tmem + (acc & 1) * kCols;
                 ok = warp_wait(&bar_free[acc & 1], (acc / 2 & 1) ^ 1, a, &s_ok);
@@ -657,7 +670,14 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                     tmem_ld32(d + c, v);
                     tc::tmem_wait_ld();
                     const int live = f < J ? t.cols - c : 0;
-                    if (pairs) {
+                    if (a.splits > 1) {
+                        float* o = a.partial + ((int64_t)t.part * a.M + t.col0 + c) * J + f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (i < live) *o = __uint_as_float(v[i]);
+                            o += J;
+                        }
+                    } else if (pairs) {
                         // neighbouring lanes exchange, so that each stores two outputs of one row: the even lane
                         // of the first of two rows, the odd lane of the second
                         uint16_t* o = out + (int64_t)(c + (lane & 1)) * J + (f & ~1);
@@ -787,7 +807,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base
     const cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * rows * size};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
-    return encode_fn()(m, type, outer ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
+    return encode_fn() && encode_fn()(m, type, outer ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -801,7 +821,7 @@ bool encode_mn(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64
     const cuuint64_t strides[3] = {(cuuint64_t)cols * 2, 128, (cuuint64_t)cols * terms * 2};
     const cuuint32_t box[4] = {64, 64, (cuuint32_t)blocks, 1};
     const cuuint32_t step[4] = {1, 1, 1, 1};
-    return encode_fn()(m, type, outer ? 4 : 3, const_cast<void*>(base), dims, strides, box, step,
+    return encode_fn() && encode_fn()(m, type, outer ? 4 : 3, const_cast<void*>(base), dims, strides, box, step,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -834,7 +854,13 @@ bool grouped_tc_supported(int dir, const GmmArgs& a) {
     return dir != kGmmDw || on16(a.out);
 }
 
-cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s) {
+int64_t grouped_tc_tiles(int64_t M, int64_t J, int* at_once) {
+    const int pair = J > kLanes;
+    *at_once = device_sms() >> pair;
+    return (J + (kLanes << pair) - 1) / (kLanes << pair) * ((M + kCols - 1) / kCols);
+}
+
+cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cudaStream_t s) {
     TcGmm p;
     p.a = a;
     const CUtensorMapDataType t = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -851,11 +877,11 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, cudaStream_t s
                     32);
         tiles *= a.G * (((int64_t)a.K + kCols - 1) / kCols);
     } else {
-        const int64_t terms = dir == kGmmFwd ? a.K : a.N;
+        const int64_t terms = pitch ? pitch : dir == kGmmFwd ? a.K : a.N;
         ok = p.wide_a ? encode_mn(&p.tma, t, a.b, a.K, a.N, a.G, 2)
                       : encode(&p.tma, t, 2, a.b, a.K, a.N, a.G, dir == kGmmFwd ? kLanes : 64);
         for (int i = 0; i < 4; ++i) ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, 16 << i);
-        tiles *= a.M / kCols + (a.off ? (int64_t)a.G : 1);
+        tiles *= (a.M / kCols + (a.off ? (int64_t)a.G : 1)) * std::max(a.splits, 1);
     }
     p.table = dir != kGmmDw && a.off && a.G <= kTable && tiles < (1 << 30);
     if (!ok) return cudaErrorInvalidValue;

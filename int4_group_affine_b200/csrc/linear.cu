@@ -436,6 +436,32 @@ __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int
     }
 }
 
+// Rows of n values, `pitch` (n rounded up to 8) apart in the copy: what TMA needs of rows it reads.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ x, int64_t pieces, int n, int pitch8,
+                                                       uint4* __restrict__ out) {
+    grid_wait();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / pitch8;
+        const int c = (int)(i - t * pitch8) * 8;
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < n ? __ldg(x + t * n + c + j) : 0;
+        out[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
+
+// The parts of split sums, added in order and rounded once.
+__global__ void __launch_bounds__(256) add_parts_kernel(const float* __restrict__ parts, int splits, int64_t n,
+                                                        uint16_t* __restrict__ y) {
+    grid_wait();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = 0.0f;
+#pragma unroll 8
+        for (int s = 0; s < splits; ++s) v += __ldg(parts + s * n + i);
+        y[i] = f2bf16(v);
+    }
+}
+
 template <int kBits, int kUnit>
 size_t codes_smem(const moe_qtensor& W, int tb, int mt) {
     const size_t ring = mt == 2 ? Slot<kBits, kUnit, 2>::kDepth * Slot<kBits, kUnit, 2>::kBytes
@@ -513,6 +539,21 @@ cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStr
     if (8 << shift != W.group) shift = -1;
     return launch_dependent(W.bits == 4 ? dequant16_kernel<4> : dequant16_kernel<8>, dim3(blocks), 256, 0, 1, s, W, pieces, shift,
                             reinterpret_cast<uint4*>(out));
+}
+
+namespace {
+unsigned blocks_for(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)device_sms() * 8); }
+}  // namespace
+
+cudaError_t launch_pad_rows(const uint16_t* x, int T, int n, uint16_t* out, cudaStream_t s) {
+    const int pitch8 = (n + 7) / 8;
+    const int64_t pieces = (int64_t)T * pitch8;
+    return launch_dependent(pad_rows_kernel, dim3(blocks_for(pieces)), 256, 0, 1, s, x, pieces, n, pitch8,
+                            reinterpret_cast<uint4*>(out));
+}
+
+cudaError_t launch_add_parts(const float* parts, int splits, int64_t n, uint16_t* y, cudaStream_t s) {
+    return launch_dependent(add_parts_kernel, dim3(blocks_for(n)), 256, 0, 1, s, parts, splits, n, y);
 }
 
 }  // namespace moeq

@@ -48,7 +48,8 @@ CASES = [(1, 512, 2048, 4, 64), (1, 1, 32, 4, 32), (1, 17, 64, 4, 64), (2, 31, 9
          (5, 33, 128, 8, 64), (7, 64, 320, 4, 64), (8, 130, 2048, 4, 32), (9, 65, 1056, 8, 32), (13, 1003, 1056, 8, 32),
          (16, 48, 384, 4, 128), (17, 257, 512, 4, 64), (33, 128, 256, 4, 32), (64, 96, 640, 8, 64),
          (65, 72, 448, 4, 64), (100, 51, 96, 4, 32), (129, 136, 1024, 4, 64), (300, 264, 576, 8, 32),
-         (1, 40, 65536, 4, 64), (3, 24, 32768, 8, 64), (2, 24, 65536, 8, 64), (5, 19, 65536, 8, 32), (17, 16, 8192, 4, 64), (2, 4099, 256, 4, 64)]
+         (1, 40, 65536, 4, 64), (3, 24, 32768, 8, 64), (2, 24, 65536, 8, 64), (5, 19, 65536, 8, 32), (17, 16, 8192, 4, 64), (2, 4099, 256, 4, 64),
+         (200, 100, 8192, 4, 64), (150, 40, 65536, 4, 64), (256, 384, 4096, 8, 32), (257, 300, 2304, 4, 128)]
 
 
 @pytest.mark.parametrize("T,N,K,bits,group", CASES)
@@ -69,7 +70,9 @@ def test_forward(T, N, K, bits, group):
 
 
 @pytest.mark.parametrize("T,N,K,bits,group", [(1, 512, 256, 4, 64), (3, 17, 64, 4, 32), (70, 136, 320, 8, 64),
-                                              (129, 1000, 96, 4, 32), (40, 1003, 128, 4, 64), (257, 264, 2048, 4, 64)])
+                                              (129, 1000, 96, 4, 32), (40, 1003, 128, 4, 64), (257, 264, 2048, 4, 64),
+                                              (50, 30011, 128, 4, 64), (300, 5000, 64, 8, 32), (1, 4099, 320, 4, 32),
+                                              (500, 3001, 1024, 4, 64)])
 def test_input_gradient(T, N, K, bits, group):
     m = _m()
     t, (s, q, b) = packed(T + N, N, K, bits, group)

@@ -60,6 +60,34 @@ def test_linear_refuses_arguments():
     assert _status(moe_affine_linear_dx, w, S, 4, D + 2, 0x60000000, 1 << 30) == 1  # dx on 16 bytes
 
 
+@pytest.mark.parametrize("N,K", [(100, 8192), (384, 4096), (4096, 2048), (1003, 256), (131072, 64), (3001, 1024)])
+def test_linear_workspace_for_some_rows_serves_fewer(N, K):
+    for f in (moe_affine_linear_workspace_bytes, moe_affine_linear_dx_workspace_bytes):
+        sizes = [f(_w(out=N, in_=K), T) for T in list(range(0, 1100, 7)) + [1500, 2048, 5000]]
+        assert sizes == sorted(sizes), (N, K)
+
+
+def _parts(T, J, terms, at_once=74):
+    """fp32 values of a split sum's parts on a 148-multiprocessor device: as many parts as there are pairs of
+    multiprocessors to a tile of 256 x 256, of at least four steps of 64 terms each."""
+    tiles, steps = -(-J // 256) * -(-T // 256), -(-terms // 64)
+    want = max(1, min(at_once // tiles, steps // 4))
+    per = -(-steps // want) * 64
+    splits = -(-terms // per)
+    return splits * T * J if splits > 1 else 0
+
+
+@pytest.mark.parametrize("T", [1, 50, 255, 256, 257, 500, 513, 1000, 3000])
+@pytest.mark.parametrize("N,K", [(3001, 1024), (100001, 256), (4096, 2048), (520, 8192), (264, 320)])
+def test_linear_workspace_holds_the_parts(T, N, K):
+    w = _w(out=N, in_=K)
+    pitch = -(-N // 8) * 8
+    need = 256 + 2 * N * K + (2 * T * pitch if pitch != N else 0) + 4 * _parts(T, K, N)
+    assert moe_affine_linear_dx_workspace_bytes(w, T) >= need
+    if moe_affine_linear_workspace_bytes(w, T) > 256:  # (few rows go by the codes)
+        assert moe_affine_linear_workspace_bytes(w, T) >= 256 + 2 * N * K + 4 * _parts(T, N, K)
+
+
 GOOD = dict(dtype=0, a=A, off=B, w=C, M=10, G=3, N=16, K=32, out=D, st=S)
 BAD = [(dict(dtype=3), 1), (dict(dtype=-1), 1), (dict(dtype=2), 2), (dict(a=None), 1), (dict(w=None), 1),
        (dict(out=None), 1), (dict(st=None), 1), (dict(off=None), 1), (dict(M=-1), 1), (dict(G=0), 1), (dict(N=0), 1),
