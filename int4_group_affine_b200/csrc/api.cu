@@ -938,7 +938,8 @@ LinearPlan linear_plan(const moe_qtensor* W, int T, bool dx) {
     const int64_t J = dx ? W->in : W->out, terms = dx ? W->out : W->in, steps = (terms + 63) / 64;
     int at_once = 1;
     const int64_t tiles = grouped_tc_tiles(std::max(T, 1), J, &at_once);
-    const int64_t want = std::max<int64_t>(1, std::min(at_once / tiles, steps / 4));
+    int64_t want = std::max<int64_t>(1, std::min(at_once / tiles, steps / 4));
+    if (steps - (steps + want - 1) / want < 16) want = 1;  // (adding parts up costs what 16 steps do, about 4 us)
     p.per = (int)((steps + want - 1) / want * 64);
     p.splits = (int)((terms + p.per - 1) / p.per);
     p.pitch = (int)((terms + 7) / 8 * 8);
@@ -977,12 +978,10 @@ moe_status linear_product(const moe_qtensor* W, bool dx, const uint16_t* rows, i
                           cudaStream_t s) {
     const LinearPlan p = linear_plan(W, T, dx);
     char* b = (char*)ws;
-    LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)(b + p.matrix), s));
     const int terms = dx ? W->out : W->in;
-    if (p.pitch != terms) {
-        LAUNCH(kPadRows, launch_pad_rows(rows, T, terms, (uint16_t*)(b + p.rows), s));
-        rows = (const uint16_t*)(b + p.rows);
-    }
+    uint16_t* padded = p.pitch != terms ? (uint16_t*)(b + p.rows) : nullptr;
+    LAUNCH(kAffineDequant, launch_affine_dequant16(*W, (uint16_t*)(b + p.matrix), rows, T, terms, padded, s));
+    if (padded) rows = padded;
     GmmArgs a;
     memset(&a, 0, sizeof(a));
     a.a = rows;

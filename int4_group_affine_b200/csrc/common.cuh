@@ -197,7 +197,7 @@ enum Kind {
     kPack, kDequant, kRouter, kTopk, kIndexCount, kIndexScan, kIndexScatter, kLoraA, kGateUp, kDown,
     kCombine, kRmsnorm, kMixedGateUp, kMixedDown, kMixedLinear, kDecode, kTcLoraGUKind, kTcGUKind,
     kTcLoraDownKind, kTcDownKind, kTcRouterKind, kKpermKind, kDecodeChain, kPrerouter, kAct8, kMixedA8, kEpDispatch, kEpCombine, kDecodeCluster,
-    kAffineLinear, kAffineDequant, kPadRows, kAddParts, kGroupedFwd, kGroupedDx, kGroupedDw, kSwiglu, kSwigluGrad, kKindCount
+    kAffineLinear, kAffineDequant, kAddParts, kGroupedFwd, kGroupedDx, kGroupedDw, kSwiglu, kSwigluGrad, kKindCount
 };
 void timing_begin(cudaStream_t s);
 void timing_mark(int kind, cudaStream_t s);
@@ -320,9 +320,10 @@ cudaError_t launch_ep_combine(const uint16_t* ret, const int32_t* pos, const flo
 // Rows times an affine-packed matrix (csrc/linear.cu): y bf16 [T][out]; the matrix as bf16 [out][in].
 bool affine_codes_supported(const moe_qtensor& W);
 cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T, uint16_t* y, cudaStream_t s);
-cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s);
-// Rows copied to a pitch of whole 16-byte pieces; fp32 parts [splits][n] added up to bf16 [n].
-cudaError_t launch_pad_rows(const uint16_t* x, int T, int n, uint16_t* out, cudaStream_t s);
+// (and, where `padded`, T rows of n values copied to a pitch of whole 16-byte pieces)
+cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, const uint16_t* rows, int T, int n,
+                                    uint16_t* padded, cudaStream_t s);
+// fp32 parts [splits][n] added up to bf16 [n]
 cudaError_t launch_add_parts(const float* parts, int splits, int64_t n, uint16_t* y, cudaStream_t s);
 
 // Products grouped by expert (csrc/grouped.cu; arguments in grouped.cuh).

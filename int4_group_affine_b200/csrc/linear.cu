@@ -375,12 +375,28 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
 // The matrix in bf16, one rounding per weight (the tensor core multiplies 16-bit operands, and the rows it meets are
 // rounded to as many bits): eight codes, one 4-bit word or two 8-bit ones, to one 16-byte store, four of them a thread
 // and step so that their loads are under way together.  Bound by the 2 bytes written per weight.
+// Beside it, rows that TMA could not read (n values each, n no multiple of 8) are copied `pitch8` 16-byte pieces apart.
 constexpr int kPieces = 4;
+struct PadRows {
+    const uint16_t* x;
+    uint4* out;
+    int64_t pieces;  // 0: none
+    int n, pitch8;
+};
 template <int kBits>
-__global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int64_t pieces, int shift, uint4* __restrict__ out) {
+__global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int64_t pieces, int shift, uint4* __restrict__ out,
+                                                        const PadRows pad) {
     const int groups8 = W.group / 8;  // 1 << shift, or shift < 0
     grid_release();  // the product's blocks set themselves up meanwhile
     grid_wait();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pad.pieces; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / pad.pitch8;
+        const int c = (int)(i - t * pad.pitch8) * 8;
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < pad.n ? __ldg(pad.x + t * pad.n + c + j) : 0;
+        pad.out[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
     for (int64_t i0 = (int64_t)blockIdx.x * (256 * kPieces) + threadIdx.x; i0 < pieces;
          i0 += (int64_t)gridDim.x * (256 * kPieces)) {
         uint32_t w[kPieces][kBits / 4];
@@ -433,20 +449,6 @@ __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int
             }
             out[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-    }
-}
-
-// Rows of n values, `pitch` (n rounded up to 8) apart in the copy: what TMA needs of rows it reads.
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ x, int64_t pieces, int n, int pitch8,
-                                                       uint4* __restrict__ out) {
-    grid_wait();
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / pitch8;
-        const int c = (int)(i - t * pitch8) * 8;
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < n ? __ldg(x + t * n + c + j) : 0;
-        out[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
 }
 
@@ -531,25 +533,21 @@ cudaError_t launch_affine_linear(const moe_qtensor& W, const uint16_t* x, int T,
     return W.bits == 4 ? launch_unit<4, 32>(a, s) : launch_unit<8, 32>(a, s);
 }
 
-cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, cudaStream_t s) {
-    const int64_t pieces = (int64_t)W.out * W.in / 8, want = (pieces + 256 * kPieces - 1) / (256 * kPieces);
-    const unsigned blocks = (unsigned)std::min<int64_t>(want, (int64_t)device_sms() * 8);
-    int shift = 0;
-    while (8 << shift < W.group) ++shift;
-    if (8 << shift != W.group) shift = -1;
-    return launch_dependent(W.bits == 4 ? dequant16_kernel<4> : dequant16_kernel<8>, dim3(blocks), 256, 0, 1, s, W, pieces, shift,
-                            reinterpret_cast<uint4*>(out));
-}
-
 namespace {
 unsigned blocks_for(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)device_sms() * 8); }
 }  // namespace
 
-cudaError_t launch_pad_rows(const uint16_t* x, int T, int n, uint16_t* out, cudaStream_t s) {
-    const int pitch8 = (n + 7) / 8;
-    const int64_t pieces = (int64_t)T * pitch8;
-    return launch_dependent(pad_rows_kernel, dim3(blocks_for(pieces)), 256, 0, 1, s, x, pieces, n, pitch8,
-                            reinterpret_cast<uint4*>(out));
+cudaError_t launch_affine_dequant16(const moe_qtensor& W, uint16_t* out, const uint16_t* rows, int T, int n,
+                                    uint16_t* padded, cudaStream_t s) {
+    const int64_t pieces = (int64_t)W.out * W.in / 8;
+    int shift = 0;
+    while (8 << shift < W.group) ++shift;
+    if (8 << shift != W.group) shift = -1;
+    PadRows pad = {};
+    if (padded) pad = {rows, reinterpret_cast<uint4*>(padded), (int64_t)T * ((n + 7) / 8), n, (n + 7) / 8};
+    const unsigned blocks = std::max(blocks_for((pieces + kPieces - 1) / kPieces), blocks_for(pad.pieces));
+    return launch_dependent(W.bits == 4 ? dequant16_kernel<4> : dequant16_kernel<8>, dim3(blocks), 256, 0, 1, s, W, pieces,
+                            shift, reinterpret_cast<uint4*>(out), pad);
 }
 
 cudaError_t launch_add_parts(const float* parts, int splits, int64_t n, uint16_t* y, cudaStream_t s) {

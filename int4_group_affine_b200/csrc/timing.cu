@@ -12,7 +12,7 @@ const char* const kNames[kKindCount] = {
     "pack", "dequant", "router_logits", "topk", "index_count", "index_scan", "index_scatter",
     "lora_a", "gate_up", "down", "combine", "rmsnorm", "mixed_gate_up", "mixed_down", "mixed_linear",
     "decode_fused", "tc_lora_gate_up", "tc_gate_up", "tc_lora_down", "tc_down", "tc_router", "kperm", "decode_chain", "prerouter", "act8", "mixed_a8", "ep_dispatch", "ep_combine", "decode_cluster",
-    "affine_linear", "affine_dequant", "pad_rows", "add_parts", "grouped_fwd", "grouped_dx", "grouped_dw", "swiglu", "swiglu_grad",
+    "affine_linear", "affine_dequant", "add_parts", "grouped_fwd", "grouped_dx", "grouped_dw", "swiglu", "swiglu_grad",
 };
 
 struct Rec {
