@@ -45,6 +45,16 @@ def _check(name, st):
         raise MoeError(name, st)
 
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _ptr(t):
     if t is None:
         return None
@@ -59,7 +69,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
+        torch = _torch or _load_torch()
         # the handle of torch.cuda.current_stream() without building the Stream object (3 us a call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
@@ -303,17 +313,16 @@ def _here(*tensors):
     current device, where another device's memory is not its own."""
     cur, out = None, []
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
             out.append(t)
             continue
         d = t.get_device()
-        if cur is None:
-            import torch
-            cur = torch.cuda.current_device() if d >= 0 else -1
-        if d < 0:
-            raise ValueError("expected a CUDA tensor")
         if d != cur:
-            raise ValueError("tensor on cuda:%d, but the current device is cuda:%d" % (d, cur))
+            if d < 0:
+                raise ValueError("expected a CUDA tensor")
+            cur = (_torch or _load_torch()).cuda.current_device()
+            if d != cur:
+                raise ValueError("tensor on cuda:%d, but the current device is cuda:%d" % (d, cur))
         if not t.is_contiguous():
             raise ValueError("expected a contiguous tensor")
         out.append(t.data_ptr())

@@ -964,7 +964,7 @@ LinearPlan linear_plan(const moe_qtensor* W, int T, bool dx) {
 // (us, codes | matrix) 2048 x 2048: 16 rows 5.5 | 12, 64 rows 12 | 12, 128 rows 17 | 12; 16384 outputs of 2048: 32 rows
 // 28 | 32, 64 rows 47 | 32; 1024 outputs of 8192: 17 rows 17 | 15, 64 rows 29 | 15, 192 rows 53 | 17.
 bool linear_matrix(const moe_qtensor* W, int T) {
-    if (!affine_codes_supported(*W)) return true;
+    if (!affine_codes_supported(*W) || T > 16384) return true;  // (a grid's height is 65535)
     if (T <= 16) return false;
     const double m = (double)W->out * W->in * 1e-6;
     const double codes = 4.0 + W->in / 1200.0 + 0.34 * m * ((T + 15) / 16);

@@ -101,7 +101,8 @@ __device__ __noinline__ void copy_edge(unsigned char* dst, const char* src, cons
     const char *begin = reinterpret_cast<const char*>(first), *end = reinterpret_cast<const char*>(last);
     if (src >= begin) {
         const int bytes = (int)min((int64_t)16, max((int64_t)0, (int64_t)(end - src)));
-        cp16((uint32_t)__cvta_generic_to_shared(dst), bytes ? src : begin, bytes);
+        const uintptr_t from = reinterpret_cast<uintptr_t>(bytes ? src : begin) & ~(uintptr_t)15;  // (an aligned one even for none)
+        cp16((uint32_t)__cvta_generic_to_shared(dst), reinterpret_cast<const void*>(from), bytes);
     } else {  // the tensor begins inside the piece
         for (int b = (int)(begin - src); b < 16 && src + b < end; b += 2)
             *reinterpret_cast<uint16_t*>(dst + b) = __ldg(reinterpret_cast<const uint16_t*>(src + b));

@@ -49,7 +49,8 @@ CASES = [(1, 512, 2048, 4, 64), (1, 1, 32, 4, 32), (1, 17, 64, 4, 64), (2, 31, 9
          (16, 48, 384, 4, 128), (17, 257, 512, 4, 64), (33, 128, 256, 4, 32), (64, 96, 640, 8, 64),
          (65, 72, 448, 4, 64), (100, 51, 96, 4, 32), (129, 136, 1024, 4, 64), (300, 264, 576, 8, 32),
          (1, 40, 65536, 4, 64), (3, 24, 32768, 8, 64), (2, 24, 65536, 8, 64), (5, 19, 65536, 8, 32), (17, 16, 8192, 4, 64), (2, 4099, 256, 4, 64),
-         (200, 100, 8192, 4, 64), (150, 40, 65536, 4, 64), (256, 384, 4096, 8, 32), (257, 300, 2304, 4, 128)]
+         (200, 100, 8192, 4, 64), (150, 40, 65536, 4, 64), (256, 384, 4096, 8, 32), (257, 300, 2304, 4, 128),
+         (16384, 3, 32, 4, 32), (70001, 1, 64, 8, 64)]
 
 
 @pytest.mark.parametrize("T,N,K,bits,group", CASES)
