@@ -51,8 +51,13 @@ _torch = None
 def _load_torch():
     global _torch
     import torch
+    torch.cuda.init()
     _torch = torch
     return torch
+
+
+def _device():
+    return (_torch or _load_torch())._C._cuda_getDevice()
 
 
 def _ptr(t):
@@ -69,9 +74,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        torch = _torch or _load_torch()
         # the handle of torch.cuda.current_stream() without building the Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        c = (_torch or _load_torch())._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -320,7 +325,7 @@ def _here(*tensors):
         if d != cur:
             if d < 0:
                 raise ValueError("expected a CUDA tensor")
-            cur = (_torch or _load_torch()).cuda.current_device()
+            cur = _device()
             if d != cur:
                 raise ValueError("tensor on cuda:%d, but the current device is cuda:%d" % (d, cur))
         if not t.is_contiguous():

@@ -880,7 +880,10 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cud
         const int64_t terms = pitch ? pitch : dir == kGmmFwd ? a.K : a.N;
         ok = p.wide_a ? encode_mn(&p.tma, t, a.b, a.K, a.N, a.G, 2)
                       : encode(&p.tma, t, 2, a.b, a.K, a.N, a.G, dir == kGmmFwd ? kLanes : 64);
-        for (int i = 0; i < 4; ++i) ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, 16 << i);
+        // the boxes that a tile of so few rows may need (each costs the caller 0.1 us)
+        const int64_t up = 16 << pair, widest = std::min<int64_t>((a.M + up - 1) / up * up, kCols) >> pair;
+        for (int i = 0; i < 4; ++i)
+            if (i == 0 || (16 << i) <= widest) ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, 16 << i);
         tiles *= (a.M / kCols + (a.off ? (int64_t)a.G : 1)) * std::max(a.splits, 1);
     }
     p.table = dir != kGmmDw && a.off && a.G <= kTable && tiles < (1 << 30);

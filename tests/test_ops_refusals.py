@@ -142,7 +142,7 @@ def test_swiglu_grad_refuses_its_own():
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
     """The binding takes contiguous tensors of the current device only (stand-in tensors: no GPU is needed)."""
-    torch = pytest.importorskip("torch")
+    import int4_group_affine_b200 as m
 
     class Tensor:
         def __init__(self, device, contiguous=True):
@@ -157,7 +157,7 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         def data_ptr(self):
             return A
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(m, "_device", lambda: 0)
     for bad, why in ((Tensor(1), "cuda:1"), (Tensor(-1), "CUDA"), (Tensor(0, False), "contiguous")):
         with pytest.raises(ValueError, match=why):
             moe_swiglu(0, bad, None, None, 0, 4, 16, D, stream=0)
