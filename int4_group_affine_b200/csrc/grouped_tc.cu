@@ -1,29 +1,42 @@
 // grouped_tc.cu - products grouped by expert with ragged sizes, and their gradients, on the tcgen05
 // tensor cores (sm_100a): operands by TMA, accumulators in tensor memory.
 //
-// One persistent kernel for the three directions.  A tile of the output is 128 matrix rows (the
-// tensor memory's lanes) by up to 256 columns, over the sum in steps of 64:
+// One persistent kernel for the three directions.  A tile of the output is 256 matrix rows (the
+// tensor memory's lanes of two blocks) by up to 256 columns, over the sum in steps of 64:
 //
 //   forward  lanes = outputs n of W[g], columns = rows m of the group, sum over k
 //   dx       lanes = inputs k of W[g],  columns = rows m of the group, sum over n
 //   dw       lanes = outputs n,         columns = inputs k,            sum over the group's rows m
 //
 // With the matrix on the lanes, the ragged side is the one whose width the instruction can choose: a
-// group of c rows takes ceil(c / 256) tiles of equal width, rounded up to 16, so a group of 17 rows
+// group of c rows takes ceil(c / 256) tiles of equal width, rounded up to 32, so a group of 17 rows
 // multiplies 32 columns and not 128.  An operand whose summed index is contiguous in memory (W and x
 // in the forward, dy in dx) is stored K-major, the others (W in dx; dy and x in dw) MN-major: the
 // 128-byte-swizzled boxes that TMA writes are the tensor core's own layout for either, so nothing is
 // transposed by hand.
 //
+// Forward and dx share a tile between a cluster's two blocks (cta_group::2): each loads its 128 lanes
+// and half of the columns, a third fewer bytes than two tiles of 128 x 256 take (7 % on 16 groups of
+// about 960 rows).  Matrices of 128 outputs or fewer, and dw, run on single blocks: in dw every tile
+// ends with a clean-up (below) that a pair has to hand across (178 us against 139).
+//
 // Rows of other groups.  The row boxes run past a group's end.  In forward and dx those rows only
 // fill columns that are not stored.  In dw they would enter the sum, so the MMA warp clears them in
 // both operands (a NaN times zero is a NaN) up to the next 16, and multiplies no further.
 //
-// Warps: 0 loads (one lane issues TMA into a ring of four 48 KB stages), 1 multiplies (one lane
-// issues tcgen05.mma), 2..9 write results, two per quarter of the lanes; the accumulator is double
-// buffered, so a tile is written while the next one multiplies.  forward and dx: a warp stores, for
-// each row m, its 32 lanes' outputs as one 64-byte piece.  dw: 32 x 128-byte boxes through shared
-// memory and TMA stores, which clip at the matrix's edges.  Every wait is bounded.
+// Warps: 0 loads (TMA into a ring of six 32 KB stages, four of 48 KB on single blocks), 1 multiplies
+// (tcgen05.mma), 2..9 write results, two per quarter of the lanes; the accumulator is double buffered,
+// so a tile is written while the next one multiplies.  Forward and dx: neighbouring lanes exchange
+// halves, and a warp stores two rows' 64-byte pieces at a time.  dw: 32 x 128-byte boxes through
+// shared memory and TMA stores, which clip at the matrix's edges.  Every wait is bounded.
+//
+// What bounds it.  The loop: a stage's products take 512 cycles at full width, and a warp issues an
+// instruction in 5 to 20 cycles, so the two pipeline warps run uniform, short loops with one elected
+// lane issuing; a pair alone steps in 0.27 us (540 cycles at 1.97 GHz), 72 pairs at once in 0.36
+// (1,690 TFLOP/s).  Whole calls: many small groups run at the speed of the memory (16,380 rows on 256
+// experts of 1024 x 2048: 183 us, 6.4 TB/s), large groups at the power limit (16 x 960 rows, fp16:
+// 68 us against 65 of the library's batched product on the same inputs), the fp32 weight gradient at
+// its stores (64 x 1024 x 2048: 136 us, 97 for the stores alone, 93 without them).
 //
 // fp32 weight gradients: the tensor core's accumulation rounds toward zero, an error that grows with
 // the sum's length (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192), so sums longer than

@@ -20,6 +20,16 @@
 // shared memory in fixed order.  Blocks stay (two per SM) and walk the matrix, each warp with a ring
 // of its own that asynchronous copies fill one to three quads (four units of a tile) ahead: x is
 // staged once per block, and the copies in flight cover the memory's latency.
+//
+// What bounds it.  Small matrices: the launch and one pass through memory (2048 x 512, one token: 3.1
+// us).  Tall ones: the integer pipe, which unpacks at half rate (2048 to 131072, one token: 36.5 us,
+// 4.1 TB/s of the packed bytes, the pipe 56 % busy; with the nibbles by two instructions instead of
+// one it took 47, with loads to registers and every tile added up by eight warps 57).
+//
+// Many rows.  dequant16_kernel writes the matrix out in bf16 and the tcgen05 kernel of the grouped
+// products multiplies it (2048 tokens, 2048 to 4096: 32 us, 6 of them for the copy).  Unpacking inside
+// that kernel, by 8 or 16 warps that fill its stages, took 38 to 47: a stage's 8192 codes cost those
+// warps more than its products cost the tensor core.
 #include <algorithm>
 
 #include "common.cuh"
