@@ -67,6 +67,7 @@ extern "C" {
 #define MOEQ_MAX_INTER 8192
 #define MOEQ_MAX_GROUPS 16384 /* groups of a grouped product */
 #define MOEQ_MAX_WIDTH 65536  /* matrix sides of the linear, grouped and SwiGLU entry points */
+#define MOEQ_MAX_ROWS (1 << 26) /* and their rows */
 
 typedef enum {
     MOE_OK = 0,
@@ -469,7 +470,7 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  *    the frozen packed weights (adapter training over the int4 base, section 二 of that page).
  * W: one matrix (n = 1) of either affine format, any `out`, group a multiple of 32 that divides
  * `in`, packed words 16-byte aligned; out, in <= MOEQ_MAX_WIDTH or MOE_ERR_UNSUPPORTED (out: up to
- * 1 << 24).  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
+ * 1 << 24), and T <= MOEQ_MAX_ROWS.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
  * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  With few rows (16, or a few times as many for
  * small matrices) the codes enter the sums as whole numbers, s and b once per group; larger T, and every
  * dx, first writes the matrix into the workspace as bf16 (one rounding per weight, at most 2^-8 of it)
@@ -477,7 +478,8 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  * or NaN input makes the outputs that depend on it infinite or NaN.
  * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses),
  * 256-byte aligned, initialised once with moe_workspace_init; it holds the status word, and
- * nothing else outlives a call.  T = 0 enqueues nothing. */
+ * nothing else outlives a call, but calls that may run at the same time (two streams, two graphs'
+ * replays) each need their own.  T = 0 enqueues nothing. */
 MOEQ_API size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T);
 MOEQ_API moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y,
                                       void* workspace, size_t ws_bytes, moe_stream stream);
@@ -506,7 +508,7 @@ MOEQ_API moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* d
  *          touched.
  *  status  device int32 word, zeroed by the caller: MOE_ERR_DEVICE_INDEX, or MOE_ERR_TIMEOUT
  *          when a bounded wait ran out (the output is then incomplete).
- * Any N and K up to MOEQ_MAX_WIDTH, G up to MOEQ_MAX_GROUPS (MOE_ERR_UNSUPPORTED beyond).  Operands that
+ * Any N and K up to MOEQ_MAX_WIDTH, M up to MOEQ_MAX_ROWS, G up to MOEQ_MAX_GROUPS (MOE_ERR_UNSUPPORTED beyond).  Operands that
  * start on 16 bytes and whose rows (x, dy, W; dw) are multiples of 16 bytes run on the tcgen05
  * kernel, others on warp-level tiles.  Results do not depend on the other groups' rows or, run to run, on
  * scheduling.  Outputs may not alias inputs.  M = 0 enqueues nothing but dw's zeros. */
@@ -529,7 +531,7 @@ MOEQ_API moe_status moe_grouped_matmul_dw(int32_t dtype, const void* dy, const v
  * (SiLU on the gate branch, as in moe_ffn_forward.)  dtype: MOE_DT_BF16 or MOE_DT_F16, of gu, h, dh
  * and dgu; w, dw fp32 [M]; w NULL: 1; dw NULL: not wanted.  Rows [offsets[0], offsets[G]) of the
  * G + 1 offsets on the device (clamped to [0, M]); offsets NULL: all M.  Other rows are neither read
- * nor written.  fp32 arithmetic, one rounding.  I <= MOEQ_MAX_WIDTH.  Outputs may not alias inputs. */
+ * nor written.  fp32 arithmetic, one rounding.  I <= MOEQ_MAX_WIDTH, M <= MOEQ_MAX_ROWS.  Outputs may not alias inputs. */
 MOEQ_API moe_status moe_swiglu(int32_t dtype, const void* gu, const float* w, const int32_t* offsets, int32_t G,
                                int32_t M, int32_t I, void* h, moe_stream stream);
 MOEQ_API moe_status moe_swiglu_grad(int32_t dtype, const void* gu, const float* w, const void* dh,

@@ -1004,7 +1004,7 @@ moe_status linear_product(const moe_qtensor* W, bool dx, const uint16_t* rows, i
 }  // namespace
 
 size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T) {
-    if (T < 0 || linear_check(W) != MOE_OK) return 0;
+    if (T < 0 || T > MOEQ_MAX_ROWS || linear_check(W) != MOE_OK) return 0;
     return T > 0 && linear_matrix(W, T) ? linear_plan(W, T, false).total : kAlign;
 }
 
@@ -1013,6 +1013,7 @@ moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T,
     moe_status st = linear_check(W);
     if (st != MOE_OK) return st;
     CHECK_ARG(T >= 0);
+    if (T > MOEQ_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
     st = ws_check(workspace, ws_bytes, moe_affine_linear_workspace_bytes(W, T));
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
@@ -1025,7 +1026,7 @@ moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T,
 }
 
 size_t moe_affine_linear_dx_workspace_bytes(const moe_qtensor* W, int32_t T) {
-    if (T < 0 || linear_check(W) != MOE_OK) return 0;
+    if (T < 0 || T > MOEQ_MAX_ROWS || linear_check(W) != MOE_OK) return 0;
     return T > 0 ? linear_plan(W, T, true).total : kAlign;
 }
 
@@ -1034,6 +1035,7 @@ moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* dy, int32_
     moe_status st = linear_check(W);
     if (st != MOE_OK) return st;
     CHECK_ARG(T >= 0);
+    if (T > MOEQ_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
     st = ws_check(workspace, ws_bytes, moe_affine_linear_dx_workspace_bytes(W, T));
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
@@ -1050,7 +1052,7 @@ moe_status grouped_check(int32_t dtype, const int32_t* offsets, int32_t M, int32
     CHECK_ARG(dtype == MOE_DT_BF16 || dtype == MOE_DT_F16 || dtype == MOE_DT_F32);
     CHECK_ARG(M >= 0 && G > 0 && N > 0 && K > 0 && (offsets || G == 1) && status);
     CHECK_ARG(aligned(offsets, 4) && aligned(status, 4));
-    if (dtype == MOE_DT_F32 || G > MOEQ_MAX_GROUPS || N > MOEQ_MAX_WIDTH || K > MOEQ_MAX_WIDTH)
+    if (dtype == MOE_DT_F32 || M > MOEQ_MAX_ROWS || G > MOEQ_MAX_GROUPS || N > MOEQ_MAX_WIDTH || K > MOEQ_MAX_WIDTH)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -1125,7 +1127,7 @@ namespace {
 moe_status swiglu_check(int32_t dtype, const float* w, const int32_t* offsets, int32_t G, int32_t M, int32_t I) {
     CHECK_ARG(dtype == MOE_DT_BF16 || dtype == MOE_DT_F16 || dtype == MOE_DT_F32);
     CHECK_ARG(M >= 0 && I > 0 && (!offsets || G > 0) && aligned(w, 4) && aligned(offsets, 4));
-    if (dtype == MOE_DT_F32 || I > MOEQ_MAX_WIDTH || (offsets && G > MOEQ_MAX_GROUPS)) return MOE_ERR_UNSUPPORTED;
+    if (dtype == MOE_DT_F32 || M > MOEQ_MAX_ROWS || I > MOEQ_MAX_WIDTH || (offsets && G > MOEQ_MAX_GROUPS)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 }  // namespace

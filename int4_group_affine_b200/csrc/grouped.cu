@@ -26,10 +26,10 @@ namespace {
 constexpr int kT = 128, kKT = 32, kThreads = 256, kAhead = 4;
 constexpr int kPitchT = kKT + 8;  // [row][term]
 constexpr int kPitchR = kT + 8;   // [term][row]
-// fp32 results: the tensor core's fp32 accumulation rounds toward zero, an error that grows with the length of the
-// sum (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192); longer sums are added up in parts of this length
-// with rounded fp32 additions.
-constexpr int kPart = 512;
+// The tensor core's fp32 accumulation rounds toward zero, an error that grows with the length of the
+// sum (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192); longer sums for fp32 results, and those that may be
+// longer than kLong16 terms for 16-bit ones, are added up in parts of this length with rounded fp32 additions.
+constexpr int kPart = 512, kLong16 = 8192;
 
 template <int kF16>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -190,7 +190,7 @@ struct Operand {
     }
 };
 
-// kParts: fp32 weight gradients (sums in parts).
+// kParts: sums in parts.
 template <int kDir, int kF16, int kParts>
 __global__ void __launch_bounds__(kThreads, kParts ? 1 : 2) gmm_any_kernel(const GmmArgs a) {
     using A = Operand<kDir == kGmmDw>;
@@ -314,13 +314,12 @@ __global__ void __launch_bounds__(kThreads, kParts ? 1 : 2) gmm_any_kernel(const
                 const int r = i0 + wi + 16 * i + g8 + 8 * (q / 2), c = j0 + wj + 8 * j + 2 * c4 + q % 2;
                 if (r >= I || c >= J) continue;
                 const int64_t at = out0 + (int64_t)r * J + c;
-                if (kParts) {
+                float v = kParts ? sum[kParts ? i : 0][j][q] : acc[i][j][q];
+                if (kParts && a.out_f32) {
                     float* o = reinterpret_cast<float*>(a.out) + at;
-                    const float v = sum[kParts ? i : 0][j][q];
                     *o = a.accumulate ? *o + v : v;
                 } else {
                     uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
-                    float v = acc[i][j][q];
                     if (kDir == kGmmDw && a.accumulate) v += from16<kF16>(*o);
                     *o = to16<kF16>(v);
                 }
@@ -346,8 +345,8 @@ cudaError_t launch_any(const GmmArgs& a, cudaStream_t s) {
     const int64_t tiles = kDir == kGmmDw ? (int64_t)a.G * ((a.N + kT - 1) / kT) * jt
                                          : ((int64_t)a.M / kT + (a.off ? a.G : 1)) * jt;
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if constexpr (kDir == kGmmDw)
-        if (a.out_f32) return launch_parts<kDir, kF16, 1>(a, (unsigned)tiles, s);
+    if ((kDir == kGmmDw && a.out_f32) || (kDir == kGmmFwd ? a.K : kDir == kGmmDx ? a.N : a.M) > kLong16)
+        return launch_parts<kDir, kF16, 1>(a, (unsigned)tiles, s);
     return launch_parts<kDir, kF16, 0>(a, (unsigned)tiles, s);
 }
 

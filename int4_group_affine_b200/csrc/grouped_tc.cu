@@ -38,10 +38,11 @@
 // 68 us against 65 of the library's batched product on the same inputs), the fp32 weight gradient at
 // its stores (64 x 1024 x 2048: 136 us, 97 for the stores alone, 93 without them).
 //
-// fp32 weight gradients: the tensor core's accumulation rounds toward zero, an error that grows with
-// the sum's length (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192), so sums longer than
-// 512 rows leave the tensor core in parts and are added by the L2's fp32 additions, one part after
-// the other (a fixed order).
+// Long sums: the tensor core's accumulation rounds toward zero, an error that grows with the sum's
+// length (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192; 4.5e-4 at 65536 of one sign, as
+// much as a rounding to fp16).  Sums of fp32 weight gradients longer than 512 rows leave the tensor
+// core in parts and are added by the L2's fp32 additions, one part after the other (a fixed order);
+// those for 16-bit results leave it every 8192 terms and are added up in fp32 by the result warps.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
@@ -62,6 +63,7 @@ constexpr int kEpi = 8;                  // result warps
 constexpr int kThreads = (2 + kEpi) * 32;
 constexpr int kOutBytes = 32 * 128;      // dw: a warp's staging box
 constexpr int kPart = 512;               // fp32 dw: terms per part
+constexpr int kPart16 = 8192;            // the others (the error of so many is a small part of their rounding)
 
 // Shared memory by direction and by the blocks that share a tile (kCta = 2: a cluster's pair, each loading its 128
 // rows and half of the columns).
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     const uint32_t sbase = tc::smem_u32(sm);
     Schedule<kDir, kCta> sched;
     sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane, good, kDir != kGmmDw && p.table && good ? &s_table : nullptr);
-    const bool parts = kDir == kGmmDw && a.out_f32;  // long sums in parts
+    const int part = kDir == kGmmDw && a.out_f32 ? kPart : kPart16;  // long sums in parts
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             if (t.g < 0) break;
             const uint32_t idesc = idesc_of<kDir, kCta>(kF16, t.width);
             for (int p0 = t.first; ok && p0 < t.terms; ++acc) {
-                const int p1 = parts ? min(t.terms, p0 + kPart) : t.terms;
+                const int p1 = min(t.terms, p0 + part);
                 const uint32_t d = tmem + (acc & 1) * kCols;
                 ok = warp_wait(&bar_free[acc & 1], (acc / 2 & 1) ^ 1, a, &s_ok);
                 if (!ok) break;
@@ -668,20 +670,46 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         const uint32_t so = tc::smem_u32(sg);
         const int J = kDir == kGmmFwd ? a.N : a.K;
         const bool pairs = J % 2 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
+        const uint32_t own = tmem + ((uint32_t)(32 * q) << 16);  // this warp's lanes
+        // Parts of a long sum before its last are added up here, kBand columns of every other band (in local memory:
+        // few sums are so long).
+        constexpr int kBand = kDir == kGmmDw ? 64 : 32;
+        float sum[kCols / 2];
         while (ok) {
             const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
+            int p0 = t.first;
+            if (kDir != kGmmDw || !a.out_f32)
+                for (; ok && t.terms - p0 > part; p0 += part, ++acc) {
+                    ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    float* to = sum;
+                    for (int c0 = kBand * half; c0 < t.cols; c0 += 2 * kBand)
+                        for (int c = c0; c < c0 + kBand; c += 32, to += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(own + (acc & 1) * kCols + c, v);
+                            tc::tmem_wait_ld();
+                            for (int j = 0; j < 32; ++j) to[j] = __uint_as_float(v[j]) + (p0 > t.first ? to[j] : 0.0f);
+                        }
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) release(&bar_free[acc & 1]);
+                }
+            if (!ok) break;
             if (kDir != kGmmDw) {
                 ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
                 if (!ok) break;
                 tc::tc_fence_after();
                 const int f = t.lane0 + kLanes * rank + 32 * q + lane;
-                const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + (acc & 1) * kCols;
+                const uint32_t d = own + (acc & 1) * kCols;
                 uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)t.col0 * J;
                 for (int c = 32 * half; c < t.cols; c += 64) {
                     uint32_t v[32];
                     tmem_ld32(d + c, v);
                     tc::tmem_wait_ld();
+                    if (p0 > t.first)
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + sum[c / 64 * 32 + j]);
                     const int live = f < J ? t.cols - c : 0;
                     if (a.splits > 1) {
                         float* o = a.partial + ((int64_t)t.part * a.M + t.col0 + c) * J + f;
@@ -722,8 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             const int per = a.out_f32 ? 32 : 64;
             const bool empty = t.terms == 0;
             if (empty && a.accumulate) continue;
-            for (int p0 = 0; ok && (p0 < t.terms || empty);) {
-                const bool add = a.accumulate || p0 > 0;
+            while (ok && (p0 < t.terms || empty)) {
+                const bool add = a.accumulate || (a.out_f32 && p0 > 0);
                 const uint32_t buf = acc & 1;
                 if (!empty) {
                     ok = warp_wait(&bar_acc[buf], (acc / 2) & 1, a, &s_ok);
@@ -736,16 +764,19 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = 0;
                     } else if (a.out_f32) {
-                        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c, w);
+                        tmem_ld32(own + buf * kCols + c, w);
                         tc::tmem_wait_ld();
                     } else {
                         uint32_t vv[2][32];
-                        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c, vv[0]);
-                        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + buf * kCols + c + 32, vv[1]);
+                        tmem_ld32(own + buf * kCols + c, vv[0]);
+                        tmem_ld32(own + buf * kCols + c + 32, vv[1]);
                         tc::tmem_wait_ld();
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t(&v)[32] = vv[h];
+                            if (p0 > 0)
+                                for (int j = 0; j < 32; ++j)
+                                    v[j] = __float_as_uint(__uint_as_float(v[j]) + sum[c / 128 * 64 + 32 * h + j]);
                             if (add) {  // the earlier gradient, added in fp32 and rounded once
                                 const uint16_t* old = reinterpret_cast<const uint16_t*>(a.out) +
                                                       ((int64_t)t.g * a.N + n) * a.K + t.col0 + c + 32 * h;
@@ -789,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) release(&bar_free[buf]);
                 ++acc;
-                p0 = parts ? p0 + kPart : t.terms;
+                p0 += part;
             }
         }
         if (kDir == kGmmDw && lane == 0) bulk_wait();  // the last boxes are read (and written) before the block ends

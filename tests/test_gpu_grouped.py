@@ -312,3 +312,36 @@ def test_on_a_given_stream():
     ref, mag, n = grouped_ref("fwd", off, x, W, dy)
     assert st == 0
     assert_within(out, ref, HALF["bf16"] * ref.abs() + 1.01 * sum_err(n, mag))
+
+
+@pytest.mark.parametrize("N,K", [(8, 8), (9, 7)])
+def test_very_many_rows_of_one_sign_in_16_bits(N, K):
+    """A million rows of one expert, all products positive, to fp16.  Parts of at most 8192
+    terms err by sum_err's 1.3e-4 of the result, the fp32 additions of at most 2048 parts, whose partial sums average
+    half of the whole, by 2048 / 2 * 2^-24 = 6e-5 at most: 2.5e-4 covers both.  In one part a sum so long would be
+    off by several half steps."""
+    M = 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(5)
+    mk = lambda n: (0.05 + 0.1 * torch.rand((M, n), generator=g, device="cuda")).half()  # noqa: E731
+    x, dy = mk(K), mk(N)
+    off = offsets_of([3, M - 10, 0, 7])
+    out, st = _run("dw", "fp16", x, dy, None, off, M, 4, N, K)
+    assert st == 0
+    ref, mag, n = grouped_ref("dw", off, x=x, dy=dy)
+    step = torch.exp2(torch.floor(torch.log2(ref.clamp(min=2.0 ** -14)))) * 2.0 ** -10
+    assert_within(out, ref, step / 2 + (2.5e-4 + 8 * 2.0 ** -23) * mag + 2.0 ** -25, "dw of many rows")
+
+
+@pytest.mark.parametrize("kind,N,K", [("fwd", 24, 65536), ("dx", 65536, 24), ("fwd", 9, 65535), ("dx", 65535, 9)])
+def test_the_longest_sums_of_one_sign(kind, N, K):
+    """As above for the widest matrices: parts of at most 8192 terms, 8 to 128 of them."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    mk = lambda *s: (0.05 + 0.1 * torch.rand(s, generator=g, device="cuda")).half()  # noqa: E731
+    off = offsets_of([5, 0, 300, 1])
+    M = int(off[-1])
+    x, dy, W = mk(M, K), mk(M, N), mk(4, N, K)
+    out, st = _run(kind, "fp16", x, dy, W, off, M, 4, N, K)
+    assert st == 0
+    ref, mag, n = grouped_ref(kind, off, x, W, dy)
+    step = torch.exp2(torch.floor(torch.log2(ref.clamp(min=2.0 ** -14)))) * 2.0 ** -10
+    assert_within(out, ref, step / 2 + (sum_err(8192, 1) + 64 * 2.0 ** -24) * mag + 2.0 ** -25, "long sums")

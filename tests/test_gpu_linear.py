@@ -157,3 +157,25 @@ def test_graph_and_stream():
         ref = x.double() @ w.t()
         assert_within(y, ref, HALF["bf16"] * ref.abs() + 1.01 * tol)
     assert m.moe_get_device_status(ws) == 0
+
+
+def test_input_gradient_through_a_million_outputs():
+    """All products positive and every weight a bf16 number, so that only the sums err: parts of up to 8192 terms by
+    sum_err's 1.3e-4 of the result, the fp32 additions of 128 of them by 128 / 2 roundings, 4e-6, then half a bf16 step.
+    (4.9e-4 covers them; in one part a sum so long would be off by more.)"""
+    m = _m()
+    N, K, T = 1 << 20, 64, 3
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w = torch.randint(-2 ** 31, 2 ** 31 - 1, (N, K // 8), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+    s, b = (torch.full((N, K // 32), v, device="cuda", dtype=torch.bfloat16) for v in (2.0 ** -4, 1.0))
+    dy = (0.5 + torch.rand((T, N), generator=g, device="cuda")).bfloat16()
+    dx = torch.empty((T, K), device="cuda", dtype=torch.bfloat16)
+    q = qtensor(m, (w, s, b), N, K, 4, 32)
+    nb = m.moe_affine_linear_dx_workspace_bytes(q, T)
+    ws = _ws(m, nb)
+    m.moe_affine_linear_dx(q, dy, T, dx, ws, nb)
+    codes = (w[:, :, None] >> (4 * torch.arange(8, device="cuda", dtype=torch.int32))) & 15
+    ref = dy.double() @ (codes.reshape(N, K).double() / 16 + 1)
+    assert m.moe_get_device_status(ws) == 0
+    step = torch.exp2(torch.floor(torch.log2(ref))) * 2.0 ** -7
+    assert_within(dx, ref, step / 2 + (4.9e-4 + 16 * 2.0 ** -23) * ref, "dx of many outputs")

@@ -47,6 +47,9 @@ def test_linear_refuses_arguments():
                     (moe_affine_linear_dx, moe_affine_linear_dx_workspace_bytes)):
         need = size(w, 4)
         assert need >= 256 and need % 256 == 0 and size(w, -1) == 0
+        assert size(w, 1 << 26) > 0 and size(w, (1 << 26) + 1) == 0
+        assert _status(f, w, S, (1 << 26) + 1, D, 0x60000000, 1 << 60) == 2
+        assert _status(f, w, S, 2 ** 31 - 1, D, 0x60000000, 1 << 60) == 2
         ws = 0x60000000
         assert _status(f, w, S, -1, D, ws, need) == 1
         assert _status(f, w, None, 4, D, ws, need) == 1
@@ -60,7 +63,8 @@ def test_linear_refuses_arguments():
     assert _status(moe_affine_linear_dx, w, S, 4, D + 2, 0x60000000, 1 << 30) == 1  # dx on 16 bytes
 
 
-@pytest.mark.parametrize("N,K", [(100, 8192), (384, 4096), (4096, 2048), (1003, 256), (131072, 64), (3001, 1024)])
+@pytest.mark.parametrize("N,K", [(100, 8192), (384, 4096), (4096, 2048), (1003, 256), (131072, 64), (3001, 1024),
+                                 (1 << 20, 2048), (1 << 22, 64)])
 def test_linear_workspace_for_some_rows_serves_fewer(N, K):
     for f in (moe_affine_linear_workspace_bytes, moe_affine_linear_dx_workspace_bytes):
         sizes = [f(_w(out=N, in_=K), T) for T in list(range(0, 1100, 7)) + [1500, 2048, 5000]]
@@ -78,7 +82,7 @@ def _parts(T, J, terms, at_once=74):
 
 
 @pytest.mark.parametrize("T", [1, 50, 255, 256, 257, 500, 513, 1000, 3000])
-@pytest.mark.parametrize("N,K", [(3001, 1024), (100001, 256), (4096, 2048), (520, 8192), (264, 320)])
+@pytest.mark.parametrize("N,K", [(3001, 1024), (100001, 256), (4096, 2048), (520, 8192), (264, 320), (1 << 20, 2048), (1 << 24, 64)])
 def test_linear_workspace_holds_the_parts(T, N, K):
     w = _w(out=N, in_=K)
     pitch = -(-N // 8) * 8
@@ -92,6 +96,7 @@ GOOD = dict(dtype=0, a=A, off=B, w=C, M=10, G=3, N=16, K=32, out=D, st=S)
 BAD = [(dict(dtype=3), 1), (dict(dtype=-1), 1), (dict(dtype=2), 2), (dict(a=None), 1), (dict(w=None), 1),
        (dict(out=None), 1), (dict(st=None), 1), (dict(off=None), 1), (dict(M=-1), 1), (dict(G=0), 1), (dict(N=0), 1),
        (dict(K=0), 1), (dict(G=16385), 2), (dict(N=65537), 2), (dict(K=65537), 2), (dict(a=A + 1), 1),
+       (dict(M=(1 << 26) + 1), 2), (dict(M=2 ** 31 - 1), 2),
        (dict(w=C + 1), 1), (dict(out=D + 1), 1), (dict(off=B + 2), 1), (dict(st=S + 2), 1), (dict(out=A), 1),
        (dict(out=C), 1)]
 
@@ -124,7 +129,7 @@ def test_no_rows_is_a_no_op():
 
 @pytest.mark.parametrize("change,status", [
     (dict(dtype=3), 1), (dict(dtype=2), 2), (dict(gu=None), 1), (dict(M=-1), 1), (dict(I=0), 1), (dict(I=65537), 2),
-    (dict(G=0), 1), (dict(G=16385), 2), (dict(w=B + 2), 1), (dict(off=C + 2), 1), (dict(gu=A + 1), 1),
+    (dict(M=(1 << 26) + 1), 2), (dict(M=2 ** 31 - 1), 2), (dict(G=0), 1), (dict(G=16385), 2), (dict(w=B + 2), 1), (dict(off=C + 2), 1), (dict(gu=A + 1), 1),
     (dict(out=None), 1), (dict(out=A), 1), (dict(out=D + 1), 1)])
 def test_swiglu_refuses(change, status):
     v = dict(dtype=0, gu=A, w=B, off=C, G=3, M=10, I=16, out=D)
