@@ -24,7 +24,8 @@
 // fill columns that are not stored.  In dw they would enter the sum, so the MMA warp clears them in
 // both operands (a NaN times zero is a NaN) up to the next 16, and multiplies no further.
 //
-// Warps: 0 loads (TMA into a ring of six 32 KB stages, four of 48 KB on single blocks), 1 multiplies
+// Warps: 0 loads (TMA, one box an operand and step, into a ring of six 32 KB stages, four of 48 KB on
+// single blocks; calls of few rows into five of two steps each, below), 1 multiplies
 // (tcgen05.mma), 2..9 write results, two per quarter of the lanes; the accumulator is double buffered,
 // so a tile is written while the next one multiplies.  Forward and dx: neighbouring lanes exchange
 // halves, and a warp stores two rows' 64-byte pieces at a time.  dw: 32 x 128-byte boxes through
@@ -32,11 +33,11 @@
 //
 // What bounds it.  The loop: a stage's products take 512 cycles at full width, and a warp issues an
 // instruction in 5 to 20 cycles, so the two pipeline warps run uniform, short loops with one elected
-// lane issuing; a pair alone steps in 0.27 us (540 cycles at 1.97 GHz), 72 pairs at once in 0.36
-// (1,690 TFLOP/s).  Whole calls: many small groups run at the speed of the memory (16,380 rows on 256
-// experts of 1024 x 2048: 183 us, 6.4 TB/s), large groups at the power limit (16 x 960 rows, fp16:
-// 68 us against 65 of the library's batched product on the same inputs), the fp32 weight gradient at
-// its stores (64 x 1024 x 2048: 136 us, 97 for the stores alone, 93 without them).
+// lane issuing, and a step's operands are one request each (with the columns in boxes of falling powers
+// of two, up to three a step, the row gradient below took 76 us).  Whole calls: many small groups run
+// at the speed of the memory (16,380 rows on 256 experts of 1024 x 2048: 177 us, 6.6 TB/s), large ones
+// at the tensor cores' and the power limit (16384 rows on 16 experts, row gradient: 68 us), the fp32
+// weight gradient at its stores (64 x 1024 x 2048: 135 us, 97 for the stores alone, 93 without them).
 //
 // Long sums: the tensor core's accumulation rounds toward zero, an error that grows with the sum's
 // length (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192; 4.5e-4 at 65536 of one sign, as
@@ -56,7 +57,7 @@ namespace {
 
 constexpr int kLanes = 128;              // matrix rows of a block's part of a tile
 constexpr int kCols = 256;               // and at most this many columns
-constexpr int kStep = 64;                // terms per stage
+constexpr int kStep = 64;                // terms per 128-byte box
 constexpr int kABytes = kLanes * 128;    // 64 16-bit terms of every lane
 constexpr int kBox = 64 * 128;           // an MN-major box: 64 terms of 64 outputs
 constexpr int kEpi = 8;                  // result warps
@@ -65,20 +66,30 @@ constexpr int kOutBytes = 32 * 128;      // dw: a warp's staging box
 constexpr int kPart = 512;               // fp32 dw: terms per part
 constexpr int kPart16 = 8192;            // the others (the error of so many is a small part of their rounding)
 
+// Calls of so few rows take stages of two steps: the ring's upkeep (300 cycles a stage) is what a block's tile of few
+// columns takes, not its products (30 cycles for 16 terms).  34 rows on 256 experts of 1024 x 2048: 24.5 us, with stages
+// of one step 26.3; 8 rows 11.9 and 13.8; 60 rows on 8 of 4096 x 4096 46 and 49 (of all that was timed one call lost:
+// the row gradient of 64 rows on 64 experts of 512 x 4096, 32.5 and 30.0).
+constexpr int kNarrowRows = 64;
+
 // Shared memory by direction and by the blocks that share a tile (kCta = 2: a cluster's pair, each loading its 128
 // rows and half of the columns).
-template <int kDir, int kCta>
+template <int kDir, int kCta, int kNarrow>
 struct Ring {
     static constexpr int outs = kDir == kGmmDw ? 1 : 0;  // a result warp's staging boxes
-    static constexpr int stages = kCta == 2 ? 6 : 4;
-    static constexpr int bytes = kABytes + kCols / kCta * 128;
+    static constexpr int steps = kNarrow ? 2 : 1;        // of a stage
+    static constexpr int stages = kNarrow ? 5 : kCta == 2 ? 6 : 4;
+    static constexpr int col_bytes = (kNarrow ? kNarrowRows : kCols) / kCta * 128;  // the columns' operand, of a step
+    static constexpr int bytes = steps * (kABytes + col_bytes);
     static constexpr size_t smem = 1024 + stages * bytes + outs * kEpi * kOutBytes;
-    static_assert(smem + (kDir == kGmmDw ? 1024 : 10 * 1024) <= 227 * 1024, "shared memory");
+    static_assert(col_bytes % 1024 == 0 && smem + (kDir == kGmmDw ? 1024 : 10 * 1024) <= 227 * 1024, "shared memory");
 };
+
+constexpr int kBoxes = 8;
 
 struct TcGmm {
     CUtensorMap tma;     // the lanes' operand
-    CUtensorMap tmb[4];  // the columns' operand: forward, dx in boxes of 16, 32, 64 and 128 rows; dw [0]
+    CUtensorMap tmb[kBoxes];  // the columns' operand: forward, dx in boxes of 1 .. 8 times 16 rows (single blocks 32); dw [0]
     CUtensorMap tmo;     // dw: the output, in boxes of 32 rows x 128 bytes
     int table;           // forward, dx: the groups fit the block's table
     int wide_a, wide_b;  // an MN-major operand whose whole tile is one box (see encode_mn)
@@ -107,12 +118,15 @@ struct Table {
     int before[kTable / 32];  // tiles before a window
 };
 
-// Fills the table (all threads of the block).
+// Fills the table (all threads of the block); false where the offsets are not in order (the table is of no use then).
 template <int kThreads>
-__device__ __forceinline__ void fill_table(Table& tb, const GmmArgs& a, int across, int tid) {
+__device__ __forceinline__ bool fill_table(Table& tb, const GmmArgs& a, int across, int tid) {
     const int warp = tid / 32, lane = tid % 32, windows = (a.G + 31) / 32;
     for (int i = tid; i <= a.G; i += kThreads) tb.off[i] = __ldg(a.off + i);
     __syncthreads();
+    bool good = true;
+    for (int i = tid; i <= a.G; i += kThreads) good = good && tb.off[i] >= (i > 0 ? tb.off[i - 1] : 0) && tb.off[i] <= a.M;
+    if (!good && blockIdx.x == 0) raise_status(a.status, MOE_ERR_DEVICE_INDEX);
     for (int w = warp; w < windows; w += kThreads / 32) {
         const int g = 32 * w + lane;
         int t = g < a.G ? (tb.off[g + 1] - tb.off[g] + kCols - 1) / kCols * across : 0;
@@ -124,7 +138,7 @@ __device__ __forceinline__ void fill_table(Table& tb, const GmmArgs& a, int acro
         tb.upto[g] = t;
         if (lane == 31) tb.before[w] = t;
     }
-    __syncthreads();
+    good = __syncthreads_and(good);
     if (warp == 0) {
         int t = lane < windows ? tb.before[lane] : 0;
 #pragma unroll
@@ -136,6 +150,7 @@ __device__ __forceinline__ void fill_table(Table& tb, const GmmArgs& a, int acro
         if (lane < windows) tb.before[lane] = lane ? t : 0;
     }
     __syncthreads();
+    return good;
 }
 
 // The group that owns `tile` (a warp; -1: none), its rows and the tile's index within it.
@@ -329,9 +344,8 @@ __device__ __forceinline__ uint32_t in_rank0(uint32_t addr) {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 template <int kCta>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {  // a warp of every block of the tile
     if (kCta == 1) {
@@ -382,17 +396,22 @@ __device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
             : "memory");
 }
 
-__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
+__device__ __forceinline__ void tma_store_3d(uint32_t one, const void* map, uint32_t src, int x, int y, int z) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n\t}" ::"l"(map),
+        "r"(src), "r"(x), "r"(y), "r"(z), "r"(one)
+        : "memory");
 }
-__device__ __forceinline__ void tma_add_3d(const void* map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     map),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
+__device__ __forceinline__ void tma_add_3d(uint32_t one, const void* map, uint32_t src, int x, int y, int z) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n\t}" ::"l"(
+            map),
+        "r"(src), "r"(x), "r"(y), "r"(z), "r"(one)
+        : "memory");
 }
+// (a whole warp's: the lanes that issue no copy have nothing to wait for)
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
@@ -483,9 +502,10 @@ struct Place {
     }
 };
 
-template <int kDir, int kF16, int kCta>
+template <int kDir, int kF16, int kCta, int kNarrow>
 __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_constant__ TcGmm p) {
-    constexpr int kStages = Ring<kDir, kCta>::stages, kStageBytes = Ring<kDir, kCta>::bytes;
+    using R = Ring<kDir, kCta, kNarrow>;
+    constexpr int kStages = R::stages, kStageBytes = R::bytes, kTerms = kStep * R::steps;  // terms of a stage
     static_assert(kDir != kGmmDw || kCta == 1, "dw clears operands behind the group's last row: a block's own");
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
@@ -517,17 +537,19 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         tc::tma_prefetch_desc(&p.tmb[0]);
         if (kDir == kGmmDw) tc::tma_prefetch_desc(&p.tmo);
     }
+    __syncwarp();
+    if (kCta == 2) cluster_arrive();
     grid_wait();
     // whether the offsets are in order, so that a group's rows need no look at the groups before it
     bool good = true;
-    if (kDir == kGmmDw || p.table) good = gmm_check_offsets(a, tid, kThreads);
-    else if (blockIdx.x == 0) (void)gmm_check_offsets(a, tid, kThreads);
     tc::tc_fence_before();
-    good = __syncthreads_and(good);
-    if constexpr (kDir != kGmmDw)
-        if (p.table && good)
-            fill_table<kThreads>(s_table, a, ((kDir == kGmmFwd ? a.N : a.K) + kLanes * kCta - 1) / (kLanes * kCta), tid);
-    if (kCta == 2) cluster_sync();
+    if (kDir != kGmmDw && p.table) {
+        good = fill_table<kThreads>(s_table, a, ((kDir == kGmmFwd ? a.N : a.K) + kLanes * kCta - 1) / (kLanes * kCta), tid);
+    } else {
+        if (kDir == kGmmDw || blockIdx.x == 0) good = gmm_check_offsets(a, tid, kThreads);
+        good = __syncthreads_and(good);
+    }
+    if (kCta == 2) cluster_wait();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
@@ -547,46 +569,44 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             if (t.g < 0) break;
             const int lanes = t.lane0 + kLanes * rank, half = t.width / kCta, col = t.col0 + half * rank;
             const int bk = (half + 63) / 64;  // dw: boxes of 64 columns
-            const uint32_t bytes = kABytes + (kDir == kGmmDw ? (p.wide_b ? kCols / 64 : bk) * kBox : half * 128);
-            for (int k = t.first; k < t.terms; k += kStep, at.next(), ++n) {
+            constexpr int kUnit = kCols / kCta / kBoxes;
+            const int units = (half + kUnit - 1) / kUnit;  // forward, dx: one box of so many rows
+            const CUtensorMap* const mapb = &p.tmb[kDir == kGmmDw ? 0 : units - 1];
+            const uint32_t bytes = R::steps * (kABytes + (kDir == kGmmDw ? (p.wide_b ? kCols / 64 : bk) * kBox : units * (kUnit * 128)));
+            for (int k0 = t.first; k0 < t.terms; k0 += kTerms, at.next(), ++n) {
                 ok = warp_wait(&bar_empty[at.st], at.phase ^ 1, a, &s_ok);  // (free from the start)
                 if (!ok) break;
-                const uint32_t sa = sbase + at.st * kStageBytes, sb = sa + kABytes, full = full0 + 8 * at.st;
+                const uint32_t full = full0 + 8 * at.st;
                 if (rank == 0) expect_tx(one, own0 + 8 * at.st, kCta * bytes);
-                if (kDir == kGmmFwd) {
-                    load_3d<kCta>(one, sa, &p.tma, k, lanes, t.g, full);
-                } else if (kDir == kGmmDx) {
-                    if (p.wide_a) {
-                        load_4d<kCta>(one, sa, &p.tma, 0, k, lanes / 64, t.g, full);
-                    } else {
-                        load_3d<kCta>(one, sa, &p.tma, lanes, k, t.g, full);
-                        load_3d<kCta>(one, sa + kBox, &p.tma, lanes + 64, k, t.g, full);
-                    }
-                } else if (p.wide_a) {
-                    load_3d<kCta>(one, sa, &p.tma, 0, t.row0 + k, lanes / 64, full);
-                } else {
-                    load_2d<kCta>(one, sa, &p.tma, lanes, t.row0 + k, full);
-                    load_2d<kCta>(one, sa + kBox, &p.tma, lanes + 64, t.row0 + k, full);
-                }
-                if (kDir == kGmmDw) {
-                    if (p.wide_b) {
-                        load_3d<kCta>(one, sb, &p.tmb[0], 0, t.row0 + k, col / 64, full);
-                    } else {
-                        for (int i = 0; i < bk; ++i)
-                            load_2d<kCta>(one, sb + i * kBox, &p.tmb[0], col + 64 * i, t.row0 + k, full);
-                    }
-                } else {  // the width in boxes of falling powers of two
-                    if (half >= 128) load_2d<kCta>(one, sb, &p.tmb[3], k, col, full);
-                    if (kCta == 1 && half == 256) {
-                        load_2d<kCta>(one, sb + 128 * 128, &p.tmb[3], k, col + 128, full);
-                    } else if (half % 128) {
-                        int row = half & 128;
 #pragma unroll
-                        for (int i = 2; i >= 0; --i)
-                            if (half & (16 << i)) {
-                                load_2d<kCta>(one, sb + row * 128, &p.tmb[i], k, col + row, full);
-                                row += 16 << i;
-                            }
+                for (int i = 0; i < R::steps; ++i) {
+                    const int k = k0 + i * kStep;  // (a second step behind the last term reads as zeros, or is not multiplied)
+                    const uint32_t sa = sbase + at.st * kStageBytes + i * kABytes;
+                    const uint32_t sb = sbase + at.st * kStageBytes + R::steps * kABytes + i * R::col_bytes;
+                    if (kDir == kGmmFwd) {
+                        load_3d<kCta>(one, sa, &p.tma, k, lanes, t.g, full);
+                    } else if (kDir == kGmmDx) {
+                        if (p.wide_a) {
+                            load_4d<kCta>(one, sa, &p.tma, 0, k, lanes / 64, t.g, full);
+                        } else {
+                            load_3d<kCta>(one, sa, &p.tma, lanes, k, t.g, full);
+                            load_3d<kCta>(one, sa + kBox, &p.tma, lanes + 64, k, t.g, full);
+                        }
+                    } else if (p.wide_a) {
+                        load_3d<kCta>(one, sa, &p.tma, 0, t.row0 + k, lanes / 64, full);
+                    } else {
+                        load_2d<kCta>(one, sa, &p.tma, lanes, t.row0 + k, full);
+                        load_2d<kCta>(one, sa + kBox, &p.tma, lanes + 64, t.row0 + k, full);
+                    }
+                    if (kDir == kGmmDw) {
+                        if (p.wide_b) {
+                            load_3d<kCta>(one, sb, &p.tmb[0], 0, t.row0 + k, col / 64, full);
+                        } else {
+                            for (int i = 0; i < bk; ++i)
+                                load_2d<kCta>(one, sb + i * kBox, &p.tmb[0], col + 64 * i, t.row0 + k, full);
+                        }
+                    } else {
+                        load_2d<kCta>(one, sb, mapb, k, col, full);
                     }
                 }
             }
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         // descriptors of stage 0; a stage, and 16 terms, are so many 16-byte units further
         constexpr uint32_t kAdvA = kDir == kGmmFwd ? 32 >> 4 : 2048 >> 4, kAdvB = kDir == kGmmDw ? 2048 >> 4 : 32 >> 4;
         const uint64_t ad0 = kDir == kGmmFwd ? tc::sdesc_k_sw128(sbase) : sdesc_mn_sw128(sbase);
-        const uint64_t bd0 = kDir == kGmmDw ? sdesc_mn_sw128(sbase + kABytes) : tc::sdesc_k_sw128(sbase + kABytes);
+        const uint64_t bd0 = kDir == kGmmDw ? sdesc_mn_sw128(sbase + kABytes) : tc::sdesc_k_sw128(sbase + R::steps * kABytes);
         const uint32_t empty0 = tc::smem_u32(bar_empty), acc0 = tc::smem_u32(bar_acc);
         const uint32_t one = elect_one();
         Place<kStages> at;
@@ -621,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 ok = warp_wait(&bar_free[acc & 1], (acc / 2 & 1) ^ 1, a, &s_ok);
                 if (!ok) break;
                 tc::tc_fence_after();
-                for (int k = p0; k < p1; k += kStep, at.next()) {
+                for (int k = p0; k < p1; k += kTerms, at.next()) {
                     ok = warp_wait(&bar_full[at.st], at.phase, a, &s_ok);
                     if (!ok) break;
                     const int left = t.terms - k;
@@ -639,13 +659,15 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                     }
                     tc::tc_fence_after();
                     const uint64_t ad = ad0 + at.st * (kStageBytes >> 4), bd = bd0 + at.st * (kStageBytes >> 4);
-                    if (left >= kStep) {
+                    auto terms16 = [&](int s) {
+                        mma<kCta>(one, d, ad + s % 4 * kAdvA + s / 4 * (kABytes >> 4),
+                                  bd + s % 4 * kAdvB + s / 4 * (R::col_bytes >> 4), idesc, s > 0 || k > p0);
+                    };
+                    if (left >= kTerms) {
 #pragma unroll
-                        for (int s = 0; s < kStep / 16; ++s)
-                            mma<kCta>(one, d, ad + s * kAdvA, bd + s * kAdvB, idesc, s > 0 || k > p0);
+                        for (int s = 0; s < kTerms / 16; ++s) terms16(s);
                     } else {
-                        for (int s = 0; 16 * s < left; ++s)
-                            mma<kCta>(one, d, ad + s * kAdvA, bd + s * kAdvB, idesc, s > 0 || k > p0);
+                        for (int s = 0; 16 * s < left; ++s) terms16(s);
                     }
                     commit<kCta>(one, empty0 + 8 * at.st);
                 }
@@ -667,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             else tc::mbar_arrive(bar);
         };
         unsigned char* sg = s_out + (warp - 2) * kOutBytes;  // dw: the staging box
-        const uint32_t so = tc::smem_u32(sg);
+        const uint32_t so = tc::smem_u32(sg), one = elect_one();
         const int J = kDir == kGmmFwd ? a.N : a.K;
         const bool pairs = J % 2 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
         const uint32_t own = tmem + ((uint32_t)(32 * q) << 16);  // this warp's lanes
@@ -798,10 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                                 w[16 * h + i] = pack16<kF16>(v[2 * i], v[2 * i + 1]);
                         }
                     }
-                    if (lane == 0) {  // the staging box is free, and earlier parts are in place
-                        if (p0 > 0) bulk_wait();
-                        else bulk_wait_read();
-                    }
+                    // the staging box is free, and earlier parts are in place
+                    if (p0 > 0) bulk_wait();
+                    else bulk_wait_read();
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -809,9 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                     tc::fence_async_smem();
                     __syncwarp();
-                    if (lane == 0 && n0 < a.N) {
-                        if (add && a.out_f32) tma_add_3d(&p.tmo, so, t.col0 + c, n0, t.g);
-                        else tma_store_3d(&p.tmo, so, t.col0 + c, n0, t.g);
+                    if (n0 < a.N) {
+                        if (add && a.out_f32) tma_add_3d(one, &p.tmo, so, t.col0 + c, n0, t.g);
+                        else tma_store_3d(one, &p.tmo, so, t.col0 + c, n0, t.g);
                         bulk_commit();
                     }
                 }
@@ -823,10 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 p0 += part;
             }
         }
-        if (kDir == kGmmDw && lane == 0) bulk_wait();  // the last boxes are read (and written) before the block ends
+        if (kDir == kGmmDw) bulk_wait();  // the last boxes are read (and written) before the block ends
     }
     __syncwarp();
-    if (kCta == 2) cluster_sync();  // (neither block ends while the other still reaches into it)
+    if (kCta == 2) cluster_arrive(), cluster_wait();  // (neither block ends while the other still reaches into it)
     else __syncthreads();
     if (warp == 1) tmem_free<kCta>(tmem, 512);
 }
@@ -870,20 +891,23 @@ bool encode_mn(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kDir, int kF16, int kCta>
+template <int kDir, int kF16, int kCta, int kNarrow>
 cudaError_t launch_cta(const TcGmm& p, int64_t tiles, cudaStream_t s) {
+    constexpr size_t smem = Ring<kDir, kCta, kNarrow>::smem;
+    constexpr auto kernel = gmm_tc_kernel<kDir, kF16, kCta, kNarrow>;
     static SmemLimit limit;
-    const cudaError_t e = limit.raise((const void*)gmm_tc_kernel<kDir, kF16, kCta>, Ring<kDir, kCta>::smem);
+    const cudaError_t e = limit.raise((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(gmm_tc_kernel<kDir, kF16, kCta>, dim3((unsigned)std::min<int64_t>(tiles, device_sms() / kCta) * kCta),
-                            kThreads, Ring<kDir, kCta>::smem, kCta, s, p);
+    return launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(tiles, device_sms() / kCta) * kCta), kThreads, smem,
+                            kCta, s, p);
 }
 
 template <int kDir, int kF16>
 cudaError_t launch_dir(const TcGmm& p, int pair, int64_t tiles, cudaStream_t s) {
     if constexpr (kDir != kGmmDw)
-        if (pair) return launch_cta<kDir, kF16, 2>(p, tiles, s);
-    return launch_cta<kDir, kF16, 1>(p, tiles, s);
+        if (pair)
+            return p.a.M <= kNarrowRows ? launch_cta<kDir, kF16, 2, 1>(p, tiles, s) : launch_cta<kDir, kF16, 2, 0>(p, tiles, s);
+    return launch_cta<kDir, kF16, 1, 0>(p, tiles, s);
 }
 
 inline bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -925,9 +949,9 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cud
         ok = p.wide_a ? encode_mn(&p.tma, t, a.b, a.K, a.N, a.G, 2)
                       : encode(&p.tma, t, 2, a.b, a.K, a.N, a.G, dir == kGmmFwd ? kLanes : 64);
         // the boxes that a tile of so few rows may need (each costs the caller 0.1 us)
-        const int64_t up = 16 << pair, widest = std::min<int64_t>((a.M + up - 1) / up * up, kCols) >> pair;
-        for (int i = 0; i < 4; ++i)
-            if (i == 0 || (16 << i) <= widest) ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, 16 << i);
+        const int unit = kCols / kBoxes >> pair;
+        for (int i = 0; i < kBoxes && (i == 0 || (i * unit << pair) < a.M); ++i)
+            ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, (i + 1) * unit);
         tiles *= (a.M / kCols + (a.off ? (int64_t)a.G : 1)) * std::max(a.splits, 1);
     }
     p.table = dir != kGmmDw && a.off && a.G <= kTable && tiles < (1 << 30);
