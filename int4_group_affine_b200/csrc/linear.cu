@@ -5,31 +5,36 @@
 // codes stay whole numbers inside a group's sum and scale and bias come once per group, so nothing
 // but the result is rounded to 16 bits.  The call is bound by the packed bytes (one token: every
 // byte is used once), so the work per byte has to stay small: the codes go through warp-level
-// tensor-core tiles (mma.sync m16n8k16: 16 matrix rows x 8 tokens), where a nibble becomes the
-// bf16 number 128 + q by one and-or of its word, eight codes in seven instructions, and the
-// products and sums cost one instruction per 256 codes.  The 128 leaves through the bias:
-// s (sum q x) + b (sum x) = s (sum (128 + q) x) + (b - 128 s) (sum x).  An 8-bit code is two
-// nibbles, lo + 16 hi, in two accumulators.  (FMAs on the CUDA cores need three instructions per
-// code and token; the tcgen05 path needs the matrix unpacked into shared or tensor memory first.)
+// tensor-core tiles (mma.sync m16n8k16: 16 matrix rows x 8 tokens), where a code masked out of its
+// word is a number already: the fp16 subnormal q 2^-24, or 16 q 2^-24 where it lies four bits higher
+// (x is divided by 16 there).  Eight 4-bit codes take five instructions, four 8-bit ones three, and
+// the products and sums one per 256 codes.  x enters as fp16 too, scaled by a power of two per unit
+// (the 64 or 32 inputs that one scale covers at least), so that the unit's largest magnitude lies in
+// [2^14, 2^15): bf16 values down to 2^-27 of that are exact, smaller ones off by 2^-35 of it at most.
+// (With nibbles as bf16 numbers 128 + q, an or more each, and bytes in two halves: one token to 131072
+// outputs 36.1 us against 34.1, 8-bit 4096 to 16384 21.3 against 18.4.  As e4m3 numbers, with x in two
+// e4m3 parts, 38.1: these products are conversions and 16-bit ones on this GPU.  FMAs on the CUDA
+// cores need three instructions per code and token; the tcgen05 path needs the matrix unpacked first.)
 //
-// A dot product does not mind the order of its terms, so a lane takes the k that lie together in
-// its words: lane (row r, quarter c) loads a unit's quarter c (a unit is the 64 or 32 inputs that
-// one scale covers at least), and the rows of x are staged in shared memory in that order, with the
-// sum of each unit beside them.  Tall matrices give every warp tiles of its own; where there are too
-// few tiles, two, four or eight warps of a block split a tile's units and add their partial sums in
-// shared memory in fixed order.  Blocks stay (two per SM) and walk the matrix, each warp with a ring
-// of its own that asynchronous copies fill one to three quads (four units of a tile) ahead: x is
-// staged once per block, and the copies in flight cover the memory's latency.
+// A dot product does not mind the order of its terms, so a lane takes the k that lie together in its
+// words: lane (row r, quarter c) loads a unit's quarter c, and the rows of x are staged in shared
+// memory in that order, with the sum and the scale of each unit beside them.  Tall matrices give
+// every warp tiles of its own; where there are too few tiles, two, four or eight warps of a block
+// split a tile's units and add their partial sums in shared memory in fixed order.  Blocks stay (two
+// per SM) and walk the matrix, each warp with a ring of its own that asynchronous copies fill one to
+// three quads (four units of a tile) ahead: x is staged once per block, and the copies in flight
+// cover the memory's latency.
 //
 // What bounds it.  Small matrices: the launch and one pass through memory (2048 x 512, one token: 3.1
-// us).  Tall ones: the integer pipe, which unpacks at half rate (2048 to 131072, one token: 36.5 us,
-// 4.1 TB/s of the packed bytes, the pipe 56 % busy; with the nibbles by two instructions instead of
-// one it took 47, with loads to registers and every tile added up by eight warps 57).
+// us).  Tall ones: the integer pipe, which unpacks at half rate (2048 to 131072, one token: 34.1 us,
+// 4.4 TB/s of the packed bytes; with loads to registers and every tile added up by eight warps 57).
 //
 // Many rows.  dequant16_kernel writes the matrix out in bf16 and the tcgen05 kernel of the grouped
 // products multiplies it (2048 tokens, 2048 to 4096: 32 us, 6 of them for the copy).  Unpacking inside
 // that kernel, by 8 or 16 warps that fill its stages, took 38 to 47: a stage's 8192 codes cost those
 // warps more than its products cost the tensor core.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -44,7 +49,7 @@ constexpr size_t kMaxSmem = 226 * 1024;
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
         "%2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -53,29 +58,41 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ void mma16816_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                            uint32_t b1) {
     asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
         "%10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Nibbles j and j + 4 of a word (j = shift / 4) as the bf16 pair {128 + q_j, 128 + q_j+4}.
-// (one three-input instruction: left to itself the compiler takes two)
-__device__ __forceinline__ uint32_t nib2(uint32_t w, int shift) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> shift), "r"(0x000F000Fu), "r"(0x43004300u));
-    return r;
+// The codes of a word as the fp16 numbers whose bits they are, the subnormals q 2^-24: pairs (0, 4) (1, 5) (2, 6) (3, 7)
+// of a 4-bit word, the second and fourth 16 times as large, or (0, 2) (1, 3) of an 8-bit one.
+template <int kBits>
+__device__ __forceinline__ uint32_t codes2(uint32_t w, int j) {
+    if (kBits == 8) return (j ? w >> 8 : w) & 0x00FF00FFu;
+    return (j & 2 ? w >> 8 : w) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
 
-// Eight bf16 values in the pair order in which the codes leave their words: a 4-bit word gives
-// (0, 4) (1, 5) (2, 6) (3, 7); the two 8-bit words give (0, 2) (1, 3), (4, 6) (5, 7).
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight bf16 values times `scale` as fp16 in the pair order in which the codes leave their words, a sixteenth of them
+// where the codes are 16 times as large.
 template <int kBits>
-__device__ __forceinline__ uint4 code_order(uint4 u) {
-    if (kBits == 4)
-        return make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
-                          __byte_perm(u.y, u.w, 0x7632));
-    return make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x5410),
-                      __byte_perm(u.z, u.w, 0x7632));
+__device__ __forceinline__ uint4 code_order(const uint4& u, float scale) {
+    const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(e[j] << 16) * scale;
+        x[2 * j + 1] = __uint_as_float(e[j] & 0xFFFF0000u) * scale;
+    }
+    if (kBits == 8)
+        return make_uint4(half_pair(x[0], x[2]), half_pair(x[1], x[3]), half_pair(x[4], x[6]), half_pair(x[5], x[7]));
+    constexpr float k16 = 0.0625f;
+    return make_uint4(half_pair(x[0], x[4]), half_pair(x[1] * k16, x[5] * k16), half_pair(x[2], x[6]),
+                      half_pair(x[3] * k16, x[7] * k16));
 }
 
 struct LinArgs {
@@ -87,6 +104,9 @@ struct LinArgs {
     int units;    // per row
     int split;    // warps that share a tile: 1, 2, 4 or 8
     int vec;      // scales and biases of four units can be loaded together
+    // of a row's 16-byte pieces: ceil(2^32 / pieces), and how far kThreads of them lead (rows, pieces)
+    uint32_t inv_chunks;
+    int step_t, step_c;
 };
 
 // A quad's words of a tile's rows in a warp's ring, in 16-byte pieces that change places by row so that the
@@ -132,6 +152,11 @@ __device__ __forceinline__ float half_of(const uint2& v, int i) {
     return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
 }
 
+// A unit's x is scaled by 2^(14 - e) for the exponent e of its largest magnitude; its product with codes q 2^-24 is
+// scaled back by 2^e, and the 2^10 that is left once at the end.
+constexpr float kBack = 0x1p10f;
+constexpr int kAhead = 4;  // pieces of x a thread has under way
+
 template <int kBits, int kUnit, int kNT, int kMT>
 __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs a) {
     using S = Slot<kBits, kUnit, kMT>;
@@ -147,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
     uint4* xs = reinterpret_cast<uint4*>(sm + kWarps * S::kDepth * S::kBytes);
     const int xunit = tb * 4 * kParts;                                             // pieces of a unit
     uint4* zeros = xs + (size_t)a.units * xunit;
-    float* xsum = reinterpret_cast<float*>(zeros + 4 * kParts);                    // [unit][tb2], then zeros
-    float* red = xsum + (size_t)a.units * tb2 + 8;                                     // [2][kWarps][kRed]
+    float* xsum = reinterpret_cast<float*>(zeros + 4 * kParts);                    // [unit][two tokens]{sums, 2^e}, then zeros
+    float* red = xsum + (size_t)a.units * tb2 * 2 + 4;                             // [2][kWarps][kRed]
     const int t0 = blockIdx.y * tb, nt = min(tb, a.T - t0);
     const int tiles = (W.out + kRows - 1) / kRows, quads = (a.units + kQuad - 1) / kQuad;
     // the block's warps: kWarps / split tiles at a time, `split` of them to a tile's units
@@ -195,28 +220,54 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
 #pragma unroll
     for (int i = 0; i < S::kDepth - 1; ++i) copy();  // under way while x is staged
 
-    // the block's tokens, in the order of the codes, and the sums of their units
+    // the block's tokens, in the order of the codes, with the scales and the sums of their units
     const int chunks = K / 8;
-    for (int i0 = 0; i0 < tb * chunks; i0 += kThreads) {
-        const int i = i0 + tid, t = i / chunks, ch = i % chunks;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (t < nt) v = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + t) * K) + ch);
-        float s = 0.0f;
-        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    int t = (int)__umulhi(tid, a.inv_chunks), ch = tid - t * chunks;
+    for (int i0 = 0; i0 < tb * chunks; i0 += kAhead * kThreads) {
+        uint4 v[kAhead];
+        int tt[kAhead], cc[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s += __uint_as_float(e[j] << 16) + __uint_as_float(e[j] & 0xFFFF0000u);
+        for (int h = 0; h < kAhead; ++h) {
+            tt[h] = t, cc[h] = ch;
+            v[h] = make_uint4(0, 0, 0, 0);
+            if (t < nt) v[h] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + t) * K) + ch);
+            t += a.step_t, ch += a.step_c;
+            if (ch >= chunks) ch -= chunks, ++t;
+        }
 #pragma unroll
-        for (int o = 1; o < kUnit / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (t < tb) {
-            const int u = ch / (kUnit / 8), in = ch % (kUnit / 8);
-            xs[u * xunit + t * 4 * kParts + ((in % kParts) ^ (kParts == 2 ? t & 1 : 0)) * 4 + in / kParts] = code_order<kBits>(v);
-            if (in == 0) xsum[u * tb2 + t] = s;
+        for (int h = 0; h < kAhead; ++h) {
+            if (i0 + h * kThreads >= tb * chunks) break;
+            float s = 0.0f;
+            const uint32_t e[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+            constexpr uint32_t k = 0x7FFF7FFFu;  // magnitudes
+            uint32_t top = __vmaxu2(__vmaxu2(e[0] & k, e[1] & k), __vmaxu2(e[2] & k, e[3] & k));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s += __uint_as_float(e[j] << 16) + __uint_as_float(e[j] & 0xFFFF0000u);
+#pragma unroll
+            for (int o = 1; o < kUnit / 8; o <<= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+                top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            if (tt[h] < tb) {
+                const int u = cc[h] / (kUnit / 8), in = cc[h] % (kUnit / 8), to = tt[h];
+                // 2^(14 - (E - 127)) for the exponent field E of the unit's largest magnitude (16 at least), which
+                // brings that to [2^14, 2^15)
+                const uint32_t E = max(max(top & 0xFFFFu, top >> 16) >> 7, 16u);
+                xs[u * xunit + to * 4 * kParts + ((in % kParts) ^ (kParts == 2 ? to & 1 : 0)) * 4 + in / kParts] =
+                    code_order<kBits>(v[h], __uint_as_float((268u - E) << 23));
+                if (in == 0) {  // (an infinity or NaN is in the sum)
+                    float* f = xsum + (u * tb2 + (to & ~1)) * 2 + (to & 1);
+                    f[0] = s / kBack;
+                    f[2] = __uint_as_float(min(E, 254u) << 23);
+                }
+            }
         }
     }
     if (tb < tb2)
-        for (int u = tid; u < a.units; u += kThreads) xsum[u * tb2 + tb] = 0.0f;
+        for (int u = tid; u < a.units; u += kThreads)
+            xsum[(u * tb2 + tb - 1) * 2 + 1] = xsum[(u * tb2 + tb - 1) * 2 + 3] = 0.0f;
     if (tid < 4 * kParts) zeros[tid] = make_uint4(0, 0, 0, 0);
-    if (tid < 8) xsum[a.units * tb2 + tid] = 0.0f;
+    if (tid < 4) xsum[a.units * tb2 * 2 + tid] = 0.0f;
     __syncthreads();
     // where this lane's pieces of x and sums start, and how far apart its units are (shared memory addresses: the
     // integer pipe that unpacks the codes has no room for address arithmetic)
@@ -230,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
             xp[n][p] = (uint32_t)__cvta_generic_to_shared(t < tb ? xs + t * 4 * kParts : zeros) +
                        ((p ^ (kParts == 2 ? t & 1 : 0)) * 4 + c) * 16;
         const bool in = 8 * n + 2 * c < tb;
-        sstep[n] = in ? tb2 * 4 : 0;
-        sp[n] = (uint32_t)__cvta_generic_to_shared(xsum + (in ? 8 * n + 2 * c : a.units * tb2));
+        sstep[n] = in ? tb2 * 8 : 0;
+        sp[n] = (uint32_t)__cvta_generic_to_shared(xsum + (in ? 8 * n + 2 * c : a.units * tb2) * 2);
     }
     uint32_t wp[kQuad];  // and its quarter of a unit's words within a slot, for the first of its rows
 #pragma unroll
@@ -284,13 +335,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                 const int u = qi * kQuad + i;
                 if (u >= a.units) break;
                 uint4 x[kNT][kParts];
-                float2 xt[kNT];
+                float4 xt[kNT];
 #pragma unroll
                 for (int n = 0; n < kNT; ++n) {
 #pragma unroll
                     for (int p = 0; p < kParts; ++p) x[n][p] = lds128(xp[n][p] + u * xstep[n]);
-                    const uint2 v = lds64(sp[n] + u * sstep[n]);
-                    xt[n] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+                    const uint4 v = lds128(sp[n] + u * sstep[n]);
+                    xt[n] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
                 }
 #pragma unroll
                 for (int m = 0; m < kMT; ++m) {
@@ -309,43 +360,29 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                         }
                     }
                     const float s0 = half_of(sc[m][0], i), s1 = half_of(sc[m][1], i);
-                    constexpr float kOff = kBits == 4 ? 128.0f : 128.0f * 17.0f;
-                    const float b0 = fmaf(-kOff, s0, half_of(bi[m][0], i)), b1 = fmaf(-kOff, s1, half_of(bi[m][1], i));
+                    const float b0 = half_of(bi[m][0], i), b1 = half_of(bi[m][1], i);
 #pragma unroll
                     for (int n = 0; n < kNT; ++n) {
-                        float lo[4], hi[4];
+                        float lo[4];
 #pragma unroll
                         for (int p = 0; p < kParts; ++p) {
                             const uint4 v = x[n][p];
-                            if constexpr (kBits == 4) {  // one word: eight codes
-                                const uint32_t w0 = w[0][p], w1 = w[1][p];
-                                if (p == 0) mma16816_0(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 4), nib2(w1, 4), v.x, v.y);
-                                else mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 4), nib2(w1, 4), v.x, v.y);
-                                mma16816(lo, nib2(w0, 8), nib2(w1, 8), nib2(w0, 12), nib2(w1, 12), v.z, v.w);
-                            } else {                     // two words: eight codes, low and high nibbles
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const uint32_t w0 = w[0][2 * p + h], w1 = w[1][2 * p + h];
-                                    const uint32_t x0 = h ? v.z : v.x, x1 = h ? v.w : v.y;
-                                    if (p == 0 && h == 0) {
-                                        mma16816_0(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 8), nib2(w1, 8), x0, x1);
-                                        mma16816_0(hi, nib2(w0, 4), nib2(w1, 4), nib2(w0, 12), nib2(w1, 12), x0, x1);
-                                    } else {
-                                        mma16816(lo, nib2(w0, 0), nib2(w1, 0), nib2(w0, 8), nib2(w1, 8), x0, x1);
-                                        mma16816(hi, nib2(w0, 4), nib2(w1, 4), nib2(w0, 12), nib2(w1, 12), x0, x1);
-                                    }
-                                }
+                            for (int h = 0; h < 2; ++h) {  // eight codes: one 4-bit word, two 8-bit ones
+                                const int j = kBits == 4 ? 2 * h : 0;
+                                const uint32_t w0 = w[0][kBits == 4 ? p : 2 * p + h], w1 = w[1][kBits == 4 ? p : 2 * p + h];
+                                const uint32_t x0 = h ? v.z : v.x, x1 = h ? v.w : v.y;
+                                const uint32_t f[4] = {codes2<kBits>(w0, j), codes2<kBits>(w1, j), codes2<kBits>(w0, j + 1),
+                                                       codes2<kBits>(w1, j + 1)};
+                                if (p == 0 && h == 0) mma16816_0(lo, f[0], f[1], f[2], f[3], x0, x1);
+                                else mma16816(lo, f[0], f[1], f[2], f[3], x0, x1);
                             }
                         }
-                        if constexpr (kBits == 8) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) lo[j] = fmaf(16.0f, hi[j], lo[j]);
-                        }
                         float(&o)[4] = y[m][n];
-                        o[0] = fmaf(s0, lo[0], fmaf(b0, xt[n].x, o[0]));
-                        o[1] = fmaf(s0, lo[1], fmaf(b0, xt[n].y, o[1]));
-                        o[2] = fmaf(s1, lo[2], fmaf(b1, xt[n].x, o[2]));
-                        o[3] = fmaf(s1, lo[3], fmaf(b1, xt[n].y, o[3]));
+                        o[0] = fmaf(s0, lo[0] * xt[n].z, fmaf(b0, xt[n].x, o[0]));
+                        o[1] = fmaf(s0, lo[1] * xt[n].w, fmaf(b0, xt[n].y, o[1]));
+                        o[2] = fmaf(s1, lo[2] * xt[n].z, fmaf(b1, xt[n].x, o[2]));
+                        o[3] = fmaf(s1, lo[3] * xt[n].w, fmaf(b1, xt[n].y, o[3]));
                     }
                 }
             }
@@ -358,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int t = 8 * n + 2 * c + j % 2, o = tile * kRows + 16 * m + g + 8 * (j / 2);
-                        if (t < nt && o < W.out) a.y[(int64_t)(t0 + t) * W.out + o] = f2bf16(y[m][n][j]);
+                        if (t < nt && o < W.out) a.y[(int64_t)(t0 + t) * W.out + o] = f2bf16(y[m][n][j] * kBack);
                     }
             continue;
         }
@@ -377,9 +414,17 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
             const int n = (tile - warp / split + at) * kRows + in % kRows;
             float v = 0.0f;
             for (int w = 0; w < split; ++w) v += rb[(at * split + w) * kRed + in];
-            if (n < W.out) a.y[(int64_t)(t0 + in / kRows) * W.out + n] = f2bf16(v);
+            if (n < W.out) a.y[(int64_t)(t0 + in / kRows) * W.out + n] = f2bf16(v * kBack);
         }
     }
+}
+
+// Nibbles j and j + 4 of a word shifted by 4 j as the bf16 pair {128 + q_j, 128 + q_j+4}.
+// (one three-input instruction: left to itself the compiler takes two)
+__device__ __forceinline__ uint32_t nib2(uint32_t w) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(0x000F000Fu), "r"(0x43004300u));
+    return r;
 }
 
 // The matrix in bf16, one rounding per weight (the tensor core multiplies 16-bit operands, and the rows it meets are
@@ -433,7 +478,7 @@ __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int
             const __nv_bfloat162 b2 = __bfloat162bfloat162(__ushort_as_bfloat16(b[j]));
             const __nv_bfloat162 k128 = __float2bfloat162_rn(128.0f);
             auto nib = [&](uint32_t v) {  // the low nibbles of bytes 0 and 2 (exact)
-                const uint32_t r = nib2(v, 0);
+                const uint32_t r = nib2(v);
                 return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r), k128);
             };
             auto affine = [&](__nv_bfloat162 q) {
@@ -478,7 +523,7 @@ template <int kBits, int kUnit>
 size_t codes_smem(const moe_qtensor& W, int tb, int mt) {
     const size_t ring = mt == 2 ? Slot<kBits, kUnit, 2>::kDepth * Slot<kBits, kUnit, 2>::kBytes
                                 : Slot<kBits, kUnit, 1>::kDepth * Slot<kBits, kUnit, 1>::kBytes;
-    return kWarps * ring + (size_t)tb * W.in * 2 + kUnit * 2 + (size_t)(W.in / kUnit) * ((tb + 1) & ~1) * 4 + 32 +
+    return kWarps * ring + (size_t)tb * W.in * 2 + kUnit * 2 + (size_t)(W.in / kUnit) * ((tb + 1) & ~1) * 8 + 16 +
            2u * kWarps * (tb > 8 ? 16 : 8) * 16 * mt * sizeof(float);
 }
 
@@ -490,7 +535,7 @@ cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     constexpr int kRows = 16 * kMT;
     const int tiles = (a.W.out + kRows - 1) / kRows, across = (a.T + a.block - 1) / a.block;
-    const int room = std::max(1, (smem > 113 * 1024 ? 1 : 2) * device_sms() / across);
+    const int room = std::max(1, (smem > 112 * 1024 ? 1 : 2) * device_sms() / across);
     // The warps that share a tile (1, 2, 4 or 8): the fewest rounds' worth of quads a warp walks, a round of shared
     // tiles costing about a quarter of a quad more for adding the parts up.  (2048 inputs, one token: 131072 outputs
     // take 36.6 us with four warps, 39.6 with one, whose second round is three quarters empty; 512 outputs need all
@@ -510,6 +555,10 @@ cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
 template <int kBits, int kUnit>
 cudaError_t launch_unit(LinArgs a, cudaStream_t s) {
     a.units = a.W.in / kUnit;
+    const int chunks = a.W.in / 8;
+    a.inv_chunks = (uint32_t)(((1ull << 32) + chunks - 1) / chunks);
+    a.step_t = kThreads / chunks;
+    a.step_c = kThreads % chunks;
     a.vec = a.W.group == kUnit && a.units % kQuad == 0 && ((uintptr_t)a.W.scales & 7) == 0 &&
             ((uintptr_t)a.W.biases & 7) == 0;
     // as many tokens a block as one or two token tiles hold and shared memory takes
@@ -519,7 +568,7 @@ cudaError_t launch_unit(LinArgs a, cudaStream_t s) {
     a.block = (a.T + blocks - 1) / blocks;
     if (a.block > 8) return launch_codes<kBits, kUnit, 2, 1>(a, s);
     // tall matrices: two row tiles a warp share the loads of x (and two blocks still fit an SM)
-    if (a.W.out >= 32 * 2 * kWarps * device_sms() && codes_smem<kBits, kUnit>(a.W, a.block, 2) <= 113 * 1024)
+    if (a.W.out >= 32 * 2 * kWarps * device_sms() && codes_smem<kBits, kUnit>(a.W, a.block, 2) <= 112 * 1024)
         return launch_codes<kBits, kUnit, 1, 2>(a, s);
     return launch_codes<kBits, kUnit, 1, 1>(a, s);
 }

@@ -30,11 +30,11 @@ def _rows(seed, T, n):
 
 
 def _forward_tol(x, s, q, b, bits, group):
-    """The larger of the two ways a call may run.  Whole codes: the products' magnitudes with the offsets the codes
-    carry (128 per nibble, so 143 per 4-bit code and 17 * 143 per 8-bit one, twice for removing it), one rounding per
-    group and term.  The matrix in bf16: half a step of every weight."""
+    """The larger of the two ways a call may run.  Whole codes: the products' magnitudes with the largest code (what x
+    loses as fp16, 2^-35 of a unit's largest value a term, is far below these), one rounding per group and term.  The
+    matrix in bf16: half a step of every weight."""
     xa, K = x.double().abs(), x.shape[1]
-    code = 2 * (143 if bits == 4 else 17 * 143)
+    code = 2 ** bits - 1
     whole = xa @ (s * code + b.abs()).t()
     w = s * q + b
     tol_codes = sum_err(K + 16 * (K // group) + 128, whole)
@@ -179,3 +179,26 @@ def test_input_gradient_through_a_million_outputs():
     assert m.moe_get_device_status(ws) == 0
     step = torch.exp2(torch.floor(torch.log2(ref))) * 2.0 ** -7
     assert_within(dx, ref, step / 2 + (4.9e-4 + 16 * 2.0 ** -23) * ref, "dx of many outputs")
+
+
+@pytest.mark.parametrize("bits,group", [(4, 32), (4, 64), (8, 64)])
+def test_rows_and_terms_of_very_different_magnitudes(bits, group):
+    """Tokens from 2^-120 to 2^120 and terms up to 2^40 apart within a row, beside zeros and subnormals; half a step of
+    the smallest bf16 numbers is 2^-134."""
+    m = _m()
+    T, N, K = 9, 70, 512
+    t, (s, q, b) = packed(8, N, K, bits, group)
+    W = qtensor(m, t, N, K, bits, group)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    p = torch.randint(-40, 1, (T, K), generator=g, device="cuda") + torch.arange(T, device="cuda")[:, None] * 30 - 120
+    x = (_rows(9, T, K).double() * torch.exp2(p.double())).bfloat16()
+    x[3] = 0
+    x[4, :group] = 0
+    x[0, ::7] = 2.0 ** -130
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    nb = m.moe_affine_linear_workspace_bytes(W, T)
+    m.moe_affine_linear(W, x, T, y, _ws(m, nb), nb)
+    tol, w = _forward_tol(x, s, q, b, bits, group)
+    ref = x.double() @ w.t()
+    assert_within(y, ref, HALF["bf16"] * ref.abs() + 1.01 * tol + 2.0 ** -134, "magnitudes")
+    assert bool((y[3] == 0).all())
