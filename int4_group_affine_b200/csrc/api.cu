@@ -961,16 +961,17 @@ LinearPlan linear_plan(const moe_qtensor* W, int T, bool dx) {
 
 // Whether a forward of T rows multiplies the matrix in bf16 (else the codes).  The codes are unpacked once for every 16
 // rows, the matrix once and written out, and its product goes through the inputs 64 at a time in every tile.  Fitted to
-// (us, codes | matrix) 2048 x 2048: 16 rows 5.5 | 12, 64 rows 12 | 12, 128 rows 17 | 12; 16384 outputs of 2048: 32 rows
-// 28 | 32, 64 rows 47 | 32; 1024 outputs of 8192: 17 rows 17 | 15, 64 rows 29 | 15, 192 rows 53 | 17.
+// (us, codes | matrix) 2048 x 2048: 17 rows 7.3 | 10.4, 64 rows 12.1 | 11.2, 128 rows 15.7 | 12.5; 16384 outputs of 2048:
+// 32 rows 27 | 29, 64 rows 45 | 29; 1024 outputs of 8192: 17 rows 16 | 14, 64 rows 27 | 15; 131072 outputs of 2048, a
+// matrix that the L2 does not hold: 32 rows 115 | 232, 48 rows 169 | 233, 64 rows 223 | 234.
 bool linear_matrix(const moe_qtensor* W, int T) {
     if (!affine_codes_supported(*W) || T > 16384) return true;  // (a grid's height is 65535)
     if (T <= 16) return false;
     const double m = (double)W->out * W->in * 1e-6;
-    const double codes = 4.0 + W->in / 1200.0 + 0.34 * m * ((T + 15) / 16);
+    const double codes = 4.0 + W->in / 1200.0 + 0.3 * m * ((T + 15) / 16);
     const double tiles = (double)((W->out + 255) / 256) * ((T + 255) / 256), waves = ceil(tiles / 74.0);
     const LinearPlan p = linear_plan(W, T, false);
-    return codes > (p.splits > 1 ? 9.5 : 6.0) + 0.28 / 64.0 * p.per * waves + 0.45 * m;
+    return codes > (p.splits > 1 ? 9.5 : 6.0) + 0.28 / 64.0 * p.per * waves + 0.45 * m + 0.4 * std::max(m - 50.0, 0.0);
 }
 
 // The matrix as bf16, then rows times it: y [T][out] of x [T][in], or dx [T][in] of dy [T][out].
