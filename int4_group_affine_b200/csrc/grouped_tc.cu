@@ -68,7 +68,7 @@ constexpr int kPart16 = 8192;            // the others (the error of so many is 
 
 // Calls of so few rows take stages of two steps: the ring's upkeep (300 cycles a stage) is what a block's tile of few
 // columns takes, not its products (30 cycles for 16 terms).  34 rows on 256 experts of 1024 x 2048: 24.5 us, with stages
-// of one step 26.3; 8 rows 11.9 and 13.8; 60 rows on 8 of 4096 x 4096 46 and 49 (of all that was timed one call lost:
+// of one step 26.3; 8 rows 11.9 and 13.8 (both less 0.9 by now); 60 rows on 8 of 4096 x 4096 46 and 49 (of all that was timed one call lost:
 // the row gradient of 64 rows on 64 experts of 512 x 4096, 32.5 and 30.0).
 constexpr int kNarrowRows = 64;
 
@@ -92,6 +92,10 @@ struct TcGmm {
     CUtensorMap tmb[kBoxes];  // the columns' operand: forward, dx in boxes of 1 .. 8 times 16 rows (single blocks 32); dw [0]
     CUtensorMap tmo;     // dw: the output, in boxes of 32 rows x 128 bytes
     int table;           // forward, dx: the groups fit the block's table
+    // forward, dx: the lane blocks of the output, and those of all parts of the sum; dw: the column blocks of a group and
+    // its tiles; and their reciprocals
+    int real, across;
+    float inv_real, inv;
     int wide_a, wide_b;  // an MN-major operand whose whole tile is one box (see encode_mn)
     GmmArgs a;
 };
@@ -116,6 +120,7 @@ struct Table {
     int off[kTable + 1];
     int upto[kTable];         // tiles up to and with a group, counted from its window of 32 groups
     int before[kTable / 32];  // tiles before a window
+    int total;
 };
 
 // Fills the table (all threads of the block); false where the offsets are not in order (the table is of no use then).
@@ -146,6 +151,7 @@ __device__ __forceinline__ bool fill_table(Table& tb, const GmmArgs& a, int acro
             const int v = __shfl_up_sync(0xffffffffu, t, o);
             if (lane >= o) t += v;
         }
+        if (lane == windows - 1) tb.total = t;
         t = __shfl_up_sync(0xffffffffu, t, 1);
         if (lane < windows) tb.before[lane] = lane ? t : 0;
     }
@@ -153,14 +159,13 @@ __device__ __forceinline__ bool fill_table(Table& tb, const GmmArgs& a, int acro
     return good;
 }
 
-// The group that owns `tile` (a warp; -1: none), its rows and the tile's index within it.
+// The group that owns `tile` (a warp; there is one), its rows and the tile's index within it.
 __device__ __forceinline__ int find_in(const Table& tb, int G, int64_t tile, int lane, GmmRows* rows, int* within) {
     const int windows = (G + 31) / 32;
     const uint32_t m = __ballot_sync(0xffffffffu, lane < windows && tile >= tb.before[min(lane, windows - 1)]);
     const int w = 31 - __clz(m), rest = (int)(tile - tb.before[w]);  // (window 0 begins with tile 0)
     const int upto = tb.upto[32 * w + lane];
     const uint32_t in = __ballot_sync(0xffffffffu, rest < upto);
-    if (in == 0) return -1;
     const int l = __ffs(in) - 1, g = 32 * w + l;
     *rows = GmmRows{tb.off[g], tb.off[g + 1]};
     *within = rest - (l > 0 ? __shfl_sync(0xffffffffu, upto, l - 1) : 0);
@@ -192,29 +197,27 @@ struct Schedule {
     int within, step, step_g;              // dw: tile within the group, and the stride in groups and tiles
     int parts, width;                      // forward, dx: tiles along the group's rows, and their width
     int64_t tile;
+    int total;                             // with a table: all tiles
     int real;                              // forward, dx: lane blocks of a part of the sum
     float inv, inv_real;
 
-    __device__ __forceinline__ void start(const GmmArgs& a, int64_t first, int64_t stride, int lane, bool good_, const Table* table_) {
+    __device__ __forceinline__ void start(const TcGmm& p, int first, int stride, int lane, bool good_, const Table* table_) {
         good = good_;
         table = table_;
+        real = p.real, across = p.across;
+        inv_real = p.inv_real, inv = p.inv;
         if (kDir == kGmmDw) {
-            across = (a.K + kCols - 1) / kCols;
-            left = (a.N + kTileLanes - 1) / kTileLanes * across;  // tiles of a group
-            g = (int)(first / left);
-            within = (int)(first % left);
-            step_g = (int)(stride / left);
-            step = (int)(stride % left);
-            fetch(a, lane);
+            left = real;  // tiles of a group
+            const Quot q = quot(first, left, inv_real), s = quot(stride, left, inv_real);
+            g = q.q, within = q.r;
+            step_g = s.q, step = s.r;
+            fetch(p.a, lane);
         } else {
-            real = ((kDir == kGmmFwd ? a.N : a.K) + kTileLanes - 1) / kTileLanes;
-            inv_real = 1.0f / (float)real;
-            across = real * max(a.splits, 1);
+            total = table ? table->total : 0;
             tile = first;
-            step = (int)stride;
+            step = stride;
             left = 0;
         }
-        inv = 1.0f / (float)across;
     }
 
     // dw: the rows of group g, on their way while the tile before them is worked on.
@@ -248,6 +251,8 @@ struct Schedule {
         } else {
             if (left <= 0) {  // another group
                 if (table) {
+                    t.g = -1;
+                    if (tile >= total) return t;
                     g = find_in(*table, a.G, tile, lane, &rows, &within);
                 } else {
                     int64_t w = 0;
@@ -341,10 +346,13 @@ __device__ __forceinline__ uint32_t in_rank0(uint32_t addr) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(0));
     return r;
 }
+// (relaxed: what the tensor memory was read for is in registers by now, and a release would wait for the stores of
+// results, which nobody in the cluster reads)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 template <int kCta>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {  // a warp of every block of the tile
@@ -539,12 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     }
     __syncwarp();
     if (kCta == 2) cluster_arrive();
+    // The next kernel may set itself up beside this one, whose blocks leave room for no second of their kind (8 rows on 64
+    // experts of 512 x 512, again and again: 5.8 us, without 6.2; kernels that share an SM crowd on its first free ones).
+    grid_release();
     grid_wait();
     // whether the offsets are in order, so that a group's rows need no look at the groups before it
     bool good = true;
     tc::tc_fence_before();
     if (kDir != kGmmDw && p.table) {
-        good = fill_table<kThreads>(s_table, a, ((kDir == kGmmFwd ? a.N : a.K) + kLanes * kCta - 1) / (kLanes * kCta), tid);
+        good = fill_table<kThreads>(s_table, a, p.across, tid);
     } else {
         if (kDir == kGmmDw || blockIdx.x == 0) good = gmm_check_offsets(a, tid, kThreads);
         good = __syncthreads_and(good);
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
     Schedule<kDir, kCta> sched;
-    sched.start(a, blockIdx.x / kCta, gridDim.x / kCta, lane, good, kDir != kGmmDw && p.table && good ? &s_table : nullptr);
+    sched.start(p, blockIdx.x / kCta, gridDim.x / kCta, lane, good, kDir != kGmmDw && p.table && good ? &s_table : nullptr);
     const int part = kDir == kGmmDw && a.out_f32 ? kPart : kPart16;  // long sums in parts
 
     if (warp == 0) {
@@ -847,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         if (kDir == kGmmDw) bulk_wait();  // the last boxes are read (and written) before the block ends
     }
     __syncwarp();
-    if (kCta == 2) cluster_arrive(), cluster_wait();  // (neither block ends while the other still reaches into it)
+    if (kCta == 2) cluster_arrive_relaxed(), cluster_wait();  // (neither block ends while the other still reaches into it)
     else __syncthreads();
     if (warp == 1) tmem_free<kCta>(tmem, 512);
 }
@@ -943,7 +954,9 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cud
              (p.wide_b ? encode_mn(&p.tmb[0], t, a.b, a.K, a.M, 0, kCols / 64) : encode(&p.tmb[0], t, 2, a.b, a.K, a.M, 0, 64)) &&
              encode(&p.tmo, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : t, a.out_f32 ? 4 : 2, a.out, a.K, a.N, a.G,
                     32);
-        tiles *= a.G * (((int64_t)a.K + kCols - 1) / kCols);
+        p.across = (a.K + kCols - 1) / kCols;
+        p.real = (int)tiles * p.across;
+        tiles = (int64_t)a.G * p.real;
     } else {
         const int64_t terms = pitch ? pitch : dir == kGmmFwd ? a.K : a.N;
         ok = p.wide_a ? encode_mn(&p.tma, t, a.b, a.K, a.N, a.G, 2)
@@ -952,8 +965,12 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cud
         const int unit = kCols / kBoxes >> pair;
         for (int i = 0; i < kBoxes && (i == 0 || (i * unit << pair) < a.M); ++i)
             ok = ok && encode(&p.tmb[i], t, 2, a.a, terms, a.M, 0, (i + 1) * unit);
-        tiles *= (a.M / kCols + (a.off ? (int64_t)a.G : 1)) * std::max(a.splits, 1);
+        p.real = (int)tiles;
+        p.across = p.real * std::max(a.splits, 1);
+        tiles = p.across * (a.M / kCols + (a.off ? (int64_t)a.G : 1));
     }
+    p.inv_real = 1.0f / (float)p.real;
+    p.inv = 1.0f / (float)p.across;
     p.table = dir != kGmmDw && a.off && a.G <= kTable && tiles < (1 << 30);
     if (!ok) return cudaErrorInvalidValue;
     switch (dir) {
