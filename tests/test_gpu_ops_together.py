@@ -220,3 +220,66 @@ def test_adapters_over_a_packed_base(T, N, K, r, A):
         assert_within(dB[a], dyd[r0].t() @ vb.v, 1.1 * (dyd[r0].abs().t() @ vb.e + sum_err(n, mag)), "dB")
         mag = (dvb.v.abs() + dvb.e).t() @ xd[r0].abs()
         assert_within(dA[a], dvb.v.t() @ xd[r0], 1.1 * (dvb.e.t() @ xd[r0].abs() + sum_err(n, mag)), "dA")
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_chain_of_calls_without_waiting(T):
+    """Each call reads what the call before wrote, the layer's own forward among them: the same bits whether the host
+    waits after every call, after none, or replays the chain as a graph (kernels set themselves up beside the one they
+    depend on)."""
+    from int4_group_affine_b200.layer import DeviceLayer
+    from synth import workloads
+    from tests.helpers import quantize_layer
+    m = _m()
+    d = DeviceLayer.from_host(workloads.TINY, quantize_layer(workloads.moe_weights(workloads.TINY, seed=3)))
+    H, rounds = d.H, 6
+    ws, nb = d.workspace(T)
+    lt, _ = packed(4, H, H, 4, 32, std=H ** -0.5)
+    lin = qtensor(m, lt, H, H, 4, 32)
+    lb = max(m.moe_affine_linear_workspace_bytes(lin, T), m.moe_affine_linear_dx_workspace_bytes(lin, T))
+    lws = torch.empty(lb, dtype=torch.uint8, device="cuda")
+    m.moe_workspace_init(lws, lb)
+    W = _randn(5, 2, 2 * H, H, std=H ** -0.5)
+    off = torch.tensor([0, T // 2, T], dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = _randn(6, T, H)
+    a, b, gu = (torch.empty((T, n), dtype=torch.bfloat16, device="cuda") for n in (H, H, 2 * H))
+    dw = torch.empty((2, 2 * H, H), device="cuda")
+
+    def chain(wait):
+        def call(f, *args):
+            f(*args)
+            if wait:
+                torch.cuda.synchronize()
+        a.copy_(x)
+        for _ in range(rounds):
+            call(m.moe_rmsnorm, a, T, H, 1e-30, b)  # (the layer's outputs are small: without it the values die out)
+            call(m.moe_ffn_forward, d.L, b, None, T, a, ws, nb)
+            call(m.moe_rmsnorm, a, T, H, 1e-30, b)
+            call(m.moe_grouped_matmul, m.DT_BF16, b, off, W, T, 2, 2 * H, H, gu, st)
+            call(m.moe_grouped_matmul_dw, m.DT_BF16, gu, b, off, T, 2, 2 * H, H, m.DT_F32, 0, dw, st)
+            call(m.moe_swiglu, m.DT_BF16, gu, None, off, 2, T, H, a)
+            call(m.moe_affine_linear, lin, a, T, b, lws, lb)
+            call(m.moe_grouped_matmul, m.DT_BF16, b, off, W, T, 2, 2 * H, H, gu, st)
+            call(m.moe_grouped_matmul_dx, m.DT_BF16, gu, off, W, T, 2, 2 * H, H, b, st)
+            call(m.moe_affine_linear_dx, lin, b, T, a, lws, lb)
+
+    chain(True)
+    want = [t.clone() for t in (a, dw)]
+    assert bool(want[0].isfinite().all()) and bool((want[0] != 0).any())
+    for _ in range(3):
+        chain(False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(want, (a, dw)))
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            chain(False)
+        for _ in range(3):
+            a.zero_()
+            dw.zero_()
+            g.replay()
+            s.synchronize()
+            assert all(torch.equal(u, v) for u, v in zip(want, (a, dw)))
+    assert int(st.item()) == 0 and m.moe_get_device_status(ws) == 0 and m.moe_get_device_status(lws) == 0
