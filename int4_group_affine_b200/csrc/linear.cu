@@ -12,7 +12,7 @@
 // (the 64 or 32 inputs that one scale covers at least), so that the unit's largest magnitude lies in
 // [2^14, 2^15): bf16 values down to 2^-27 of that are exact, smaller ones off by 2^-35 of it at most.
 // (With nibbles as bf16 numbers 128 + q, an or more each, and bytes in two halves: one token to 131072
-// outputs 36.1 us against 34.1, 8-bit 4096 to 16384 21.3 against 18.4.  As e4m3 numbers, with x in two
+// outputs 36.1 us against 34.1 at the time, 8-bit 4096 to 16384 21.3 against 18.4.  As e4m3 numbers, with x in two
 // e4m3 parts, 38.1: these products are conversions and 16-bit ones on this GPU.  FMAs on the CUDA
 // cores need three instructions per code and token; the tcgen05 path needs the matrix unpacked first.)
 //
@@ -26,8 +26,8 @@
 // cover the memory's latency.
 //
 // What bounds it.  Small matrices: the launch and one pass through memory (2048 x 512, one token: 3.1
-// us).  Tall ones: the integer pipe, which unpacks at half rate (2048 to 131072, one token: 34.1 us,
-// 4.4 TB/s of the packed bytes; with loads to registers and every tile added up by eight warps 57).
+// us).  Tall ones: the integer pipe, which unpacks at half rate (2048 to 131072, one token: 33.0 us,
+// 4.6 TB/s of the packed bytes; with loads to registers and every tile added up by eight warps 57).
 //
 // Many rows.  dequant16_kernel writes the matrix out in bf16 and the tcgen05 kernel of the grouped
 // products multiplies it (2048 tokens, 2048 to 4096: 32 us, 6 of them for the copy).  Unpacking inside
@@ -103,7 +103,7 @@ struct LinArgs {
     int block;    // tokens of a block (<= 8 kNT)
     int units;    // per row
     int split;    // warps that share a tile: 1, 2, 4 or 8
-    int vec;      // scales and biases of four units can be loaded together
+    uint32_t inv_span;  // ceil(2^32 / units of a group), 0 for one
     // of a row's 16-byte pieces: ceil(2^32 / pieces), and how far kThreads of them lead (rows, pieces)
     uint32_t inv_chunks;
     int step_t, step_c;
@@ -136,6 +136,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -157,7 +160,8 @@ __device__ __forceinline__ float half_of(const uint2& v, int i) {
 constexpr float kBack = 0x1p10f;
 constexpr int kAhead = 4;  // pieces of x a thread has under way
 
-template <int kBits, int kUnit, int kNT, int kMT>
+// kVec: the scales and biases of four units can be copied together.
+template <int kBits, int kUnit, int kNT, int kMT, int kVec>
 __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs a) {
     using S = Slot<kBits, kUnit, kMT>;
     constexpr int kParts = kUnit / 32;   // 16-byte pieces of x per lane and unit
@@ -187,7 +191,18 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
     constexpr int kStep = 32 / S::kPieces;
     const int crow = lane / S::kPieces, cp = lane % S::kPieces;
     int ctile = first, cq = q0, cslot = 0;
+    // Scales and biases that no aligned copy fetches are loaded one quad's work before they are stored beside the codes
+    // (loaded where they are used instead: 2880 inputs to 19168, one token 17.3 us against 14.3).
+    uint32_t pend[kMT][kQuad];
+    int pslot = -1;
     auto copy = [&]() {
+        if (!kVec && pslot >= 0) {
+            const uint32_t dst = sring + pslot * S::kBytes + kRows * S::kPieces * 16 + lane * 8;
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+                sts64(dst + m * 256, pend[m][0] | pend[m][1] << 16, pend[m][2] | pend[m][3] << 16);
+            pslot = -1;
+        }
         if (ctile < tiles && cq < q1) {
             const uint32_t dst = sring + cslot * S::kBytes;
             const char* src = reinterpret_cast<const char*>(W.packed) + (int64_t)ctile * kRows * row_bytes +
@@ -205,11 +220,23 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                     cp16(dst + S::piece(i * kStep + crow, cp) * 16,
                          src + min(i * kStep + crow, last) * row_bytes + (cp < left ? cp * 16 : 0), cp < left ? 16 : 0);
             }
-            if (a.vec) {  // lane: row lane / 2 (and 16 further), its scales or its biases
-                const uint16_t* sb = (lane & 1 ? W.biases : W.scales) + (int64_t)ctile * kRows * groups + cq * kQuad;
+            // lane: row lane / 2 (and 16 further), its scales or its biases
+            const uint16_t* sb = (lane & 1 ? W.biases : W.scales) + (int64_t)ctile * kRows * groups;
+            if (kVec) {
+                sb += cq * kQuad;
 #pragma unroll
                 for (int m = 0; m < kMT; ++m)
                     cp8(dst + kRows * S::kPieces * 16 + (m * 32 + lane) * 8, sb + min(m * 16 + lane / 2, last) * groups, 8);
+            }
+            if (!kVec) {
+                pslot = cslot;
+#pragma unroll
+                for (int i = 0; i < kQuad; ++i) {
+                    const uint32_t u = min(cq * kQuad + i, a.units - 1), gi = a.inv_span ? __umulhi(u, a.inv_span) : u;
+#pragma unroll
+                    for (int m = 0; m < kMT; ++m)
+                        pend[m][i] = __ldg(sb + (int64_t)min(m * 16 + lane / 2, last) * groups + gi);
+                }
             }
             if (++cq == q1) cq = q0, ctile += stride;
             if (++cslot == S::kDepth) cslot = 0;
@@ -302,33 +329,17 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                 for (int j = 0; j < 4; ++j) y[m][n][j] = 0.0f;
         for (int qi = q0; qi < q1 && tile < tiles; ++qi) {
             uint2 sc[kMT][2], bi[kMT][2];  // scales and biases of the quad, bf16 pairs
-            if (!a.vec) {
-#pragma unroll
-                for (int r = 0; r < 2 * kMT; ++r) {
-                    const int64_t at = (int64_t)min(tile * kRows + g + 8 * r, W.out - 1) * groups;
-                    uint32_t e[2][kQuad];
-#pragma unroll
-                    for (int i = 0; i < kQuad; ++i) {
-                        const int gi = min(qi * kQuad + i, a.units - 1) * kUnit / W.group;
-                        e[0][i] = __ldg(W.scales + at + gi);
-                        e[1][i] = __ldg(W.biases + at + gi);
-                    }
-                    sc[r / 2][r % 2] = make_uint2(e[0][0] | e[0][1] << 16, e[0][2] | e[0][3] << 16);
-                    bi[r / 2][r % 2] = make_uint2(e[1][0] | e[1][1] << 16, e[1][2] | e[1][3] << 16);
-                }
-            }
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kDepth - 2) : "memory");
             __syncwarp();
             copy();  // into the slot of the quad before this one
             const uint32_t q = sring + slot * S::kBytes;
             if (++slot == S::kDepth) slot = 0;
-            if (a.vec) {
+            if (!kVec) __syncwarp();
 #pragma unroll
-                for (int r = 0; r < 2 * kMT; ++r) {
-                    const uint4 v = lds128(q + cp_s + 8 * r * 16);
-                    sc[r / 2][r % 2] = make_uint2(v.x, v.y);
-                    bi[r / 2][r % 2] = make_uint2(v.z, v.w);
-                }
+            for (int r = 0; r < 2 * kMT; ++r) {
+                const uint4 v = lds128(q + cp_s + 8 * r * 16);
+                sc[r / 2][r % 2] = make_uint2(v.x, v.y);
+                bi[r / 2][r % 2] = make_uint2(v.z, v.w);
             }
 #pragma unroll
             for (int i = 0; i < kQuad; ++i) {
@@ -527,11 +538,12 @@ size_t codes_smem(const moe_qtensor& W, int tb, int mt) {
            2u * kWarps * (tb > 8 ? 16 : 8) * 16 * mt * sizeof(float);
 }
 
-template <int kBits, int kUnit, int kNT, int kMT>
-cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
+template <int kBits, int kUnit, int kNT, int kMT, int kVec>
+cudaError_t launch_vec(LinArgs a, cudaStream_t s) {
     const size_t smem = codes_smem<kBits, kUnit>(a.W, a.block, kMT);
     static SmemLimit limit;
-    const cudaError_t e = limit.raise((const void*)linear_codes_kernel<kBits, kUnit, kNT, kMT>, kMaxSmem);
+    constexpr auto kernel = linear_codes_kernel<kBits, kUnit, kNT, kMT, kVec>;
+    const cudaError_t e = limit.raise((const void*)kernel, kMaxSmem);
     if (e != cudaSuccess) return e;
     constexpr int kRows = 16 * kMT;
     const int tiles = (a.W.out + kRows - 1) / kRows, across = (a.T + a.block - 1) / a.block;
@@ -548,19 +560,24 @@ cudaError_t launch_codes(LinArgs a, cudaStream_t s) {
         if (cost < best) best = cost, a.split = s;
     }
     const int per = kWarps / a.split, want = (tiles + per - 1) / per;
-    return launch_dependent(linear_codes_kernel<kBits, kUnit, kNT, kMT>, dim3(std::min(want, room), across), kThreads, smem,
-                            1, s, a);
+    return launch_dependent(kernel, dim3(std::min(want, room), across), kThreads, smem, 1, s, a);
+}
+
+template <int kBits, int kUnit, int kNT, int kMT>
+cudaError_t launch_codes(const LinArgs& a, cudaStream_t s) {
+    const bool vec = a.W.group == kUnit && a.units % kQuad == 0 && (((uintptr_t)a.W.scales | (uintptr_t)a.W.biases) & 7) == 0;
+    return vec ? launch_vec<kBits, kUnit, kNT, kMT, 1>(a, s) : launch_vec<kBits, kUnit, kNT, kMT, 0>(a, s);
 }
 
 template <int kBits, int kUnit>
 cudaError_t launch_unit(LinArgs a, cudaStream_t s) {
     a.units = a.W.in / kUnit;
+    const uint32_t span = a.W.group / kUnit;
+    a.inv_span = span > 1 ? (uint32_t)(((1ull << 32) + span - 1) / span) : 0;
     const int chunks = a.W.in / 8;
     a.inv_chunks = (uint32_t)(((1ull << 32) + chunks - 1) / chunks);
     a.step_t = kThreads / chunks;
     a.step_c = kThreads % chunks;
-    a.vec = a.W.group == kUnit && a.units % kQuad == 0 && ((uintptr_t)a.W.scales & 7) == 0 &&
-            ((uintptr_t)a.W.biases & 7) == 0;
     // as many tokens a block as one or two token tiles hold and shared memory takes
     int tb = std::min(a.T, 16);
     while (tb > 1 && codes_smem<kBits, kUnit>(a.W, tb, 1) > kMaxSmem) --tb;

@@ -202,3 +202,23 @@ def test_rows_and_terms_of_very_different_magnitudes(bits, group):
     ref = x.double() @ w.t()
     assert_within(y, ref, HALF["bf16"] * ref.abs() + 1.01 * tol + 2.0 ** -134, "magnitudes")
     assert bool((y[3] == 0).all())
+
+
+@pytest.mark.parametrize("T,N,K,bits,group", [(1, 100, 1024, 4, 64), (9, 4800, 512, 8, 64), (2, 5000, 1024, 4, 256)])
+def test_scales_and_biases_at_any_address(T, N, K, bits, group):
+    """Scales and biases that start on an odd 16-bit element give the same bits as aligned ones."""
+    m = _m()
+    t, _ = packed(10, N, K, bits, group)
+    x, out = _rows(11, T, K), []
+    for shift in (0, 1):
+        moved = []
+        for v in t[1:]:
+            room = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")
+            room[shift:shift + v.numel()] = v.flatten()
+            moved.append(room[shift:])
+        W = qtensor(m, (t[0], *moved), N, K, bits, group)
+        nb = m.moe_affine_linear_workspace_bytes(W, T)
+        y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+        m.moe_affine_linear(W, x, T, y, _ws(m, nb), nb)
+        out.append(y)
+    assert torch.equal(*out)
