@@ -190,8 +190,21 @@ struct Operand {
     }
 };
 
-// kParts: sums in parts.
-template <int kDir, int kF16, int kParts>
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of the cluster's block `rank`, at this block's shared memory address `addr`.
+__device__ __forceinline__ float ld_of(uint32_t addr, int rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// kParts: sums in parts.  kSplit: a cluster's a.splits blocks share a tile's sum (weight gradients).
+template <int kDir, int kF16, int kParts, int kSplit>
 __global__ void __launch_bounds__(kThreads, kParts ? 1 : 2) gmm_any_kernel(const GmmArgs a) {
     using A = Operand<kDir == kGmmDw>;
     using B = Operand<kDir != kGmmFwd>;
@@ -207,11 +220,17 @@ __global__ void __launch_bounds__(kThreads, kParts ? 1 : 2) gmm_any_kernel(const
     const int jt = (J + kT - 1) / kT;
     int g, i0, j0, I, S;
     GmmRows rows;
+    const int rank = kSplit ? blockIdx.x % a.splits : 0;
     if (kDir == kGmmDw) {
-        const int it = (a.N + kT - 1) / kT;
-        g = (int)(blockIdx.x / ((int64_t)it * jt));
-        const int rem = (int)(blockIdx.x % ((int64_t)it * jt));
+        const int it = (a.N + kT - 1) / kT, tile = kSplit ? blockIdx.x / a.splits : blockIdx.x;
+        g = (int)(tile / ((int64_t)it * jt));
+        const int rem = (int)(tile % ((int64_t)it * jt));
         rows = gmm_rows_of(a, g, lane);
+        if (kSplit) {  // this block's rows, whole steps
+            const int steps = (rows.end - rows.begin + kKT - 1) / kKT, per = (steps + a.splits - 1) / a.splits * kKT;
+            rows.begin = min(rows.begin + rank * per, rows.end);
+            rows.end = min(rows.begin + per, rows.end);
+        }
         i0 = rem / jt * kT;
         j0 = rem % jt * kT;
         I = a.N;
@@ -305,37 +324,63 @@ __global__ void __launch_bounds__(kThreads, kParts ? 1 : 2) gmm_any_kernel(const
     }
 
     const int64_t out0 = kDir == kGmmDw ? g * nk : (int64_t)rows.begin * J;
+    auto store = [&](int i, int j, int q, float v) {
+        const int r = i0 + wi + 16 * i + g8 + 8 * (q / 2), c = j0 + wj + 8 * j + 2 * c4 + q % 2;
+        if (r >= I || c >= J) return;
+        const int64_t at = out0 + (int64_t)r * J + c;
+        if (kParts && a.out_f32) {
+            float* o = reinterpret_cast<float*>(a.out) + at;
+            *o = a.accumulate ? *o + v : v;
+        } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
+            if (kDir == kGmmDw && a.accumulate) v += from16<kF16>(*o);
+            *o = to16<kF16>(v);
+        }
+    };
+    float* sv = reinterpret_cast<float*>(sm);  // kSplit: [value of a thread][thread], over the copies
+    if (kSplit) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int r = i0 + wi + 16 * i + g8 + 8 * (q / 2), c = j0 + wj + 8 * j + 2 * c4 + q % 2;
-                if (r >= I || c >= J) continue;
-                const int64_t at = out0 + (int64_t)r * J + c;
-                float v = kParts ? sum[kParts ? i : 0][j][q] : acc[i][j][q];
-                if (kParts && a.out_f32) {
-                    float* o = reinterpret_cast<float*>(a.out) + at;
-                    *o = a.accumulate ? *o + v : v;
-                } else {
-                    uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + at;
-                    if (kDir == kGmmDw && a.accumulate) v += from16<kF16>(*o);
-                    *o = to16<kF16>(v);
-                }
+                const float v = kParts ? sum[kParts ? i : 0][j][q] : acc[i][j][q];
+                if (kSplit) sv[((i * 4 + j) * 4 + q) * kThreads + tid] = v;
+                else store(i, j, q, v);
             }
+    if (kSplit) {  // every block adds up its share of the values, in the blocks' order
+        static_assert(64 * kThreads * 4 <= kAhead * kRaw, "the values take the copies' place");
+        cluster_sync();
+        const uint32_t base = (uint32_t)__cvta_generic_to_shared(sv + tid);
+        const int share = 64 / a.splits;
+        for (int e = rank * share; e < (rank + 1) * share; ++e) {
+            float part[8], v = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) part[b] = b < a.splits ? ld_of(base + e * (kThreads * 4), b) : 0.0f;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) v += part[b];
+            store(e / 16, e / 4 % 4, e % 4, v);
+        }
+        cluster_sync();  // (no block ends while another reads it)
+    }
 }
 
-template <int kDir, int kF16, int kParts>
+template <int kDir, int kF16, int kParts, int kSplit>
 cudaError_t launch_parts(const GmmArgs& a, unsigned tiles, cudaStream_t s) {
     using A = Operand<kDir == kGmmDw>;
     using B = Operand<kDir != kGmmFwd>;
     constexpr size_t smem = kAhead * (A::kRaw + B::kRaw) + (A::kElems + B::kElems) * 2;
     static_assert(2 * smem <= 227 * 1024 - 2048, "two blocks a multiprocessor");
     static SmemLimit limit;
-    const cudaError_t e = limit.raise((const void*)gmm_any_kernel<kDir, kF16, kParts>, smem);
+    constexpr auto kernel = gmm_any_kernel<kDir, kF16, kParts, kSplit>;
+    const cudaError_t e = limit.raise((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(gmm_any_kernel<kDir, kF16, kParts>, dim3(tiles), kThreads, smem, 1, s, a);
+    const int cluster = kSplit ? a.splits : 1;
+    return launch_dependent(kernel, dim3(tiles * cluster), kThreads, smem, cluster, s, a);
 }
 
 template <int kDir, int kF16>
@@ -345,20 +390,34 @@ cudaError_t launch_any(const GmmArgs& a, cudaStream_t s) {
     const int64_t tiles = kDir == kGmmDw ? (int64_t)a.G * ((a.N + kT - 1) / kT) * jt
                                          : ((int64_t)a.M / kT + (a.off ? a.G : 1)) * jt;
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if constexpr (kDir == kGmmDw)
+        if (a.splits > 1) return launch_parts<kDir, kF16, 1, 1>(a, (unsigned)tiles, s);
     if ((kDir == kGmmDw && a.out_f32) || (kDir == kGmmFwd ? a.K : kDir == kGmmDx ? a.N : a.M) > kLong16)
-        return launch_parts<kDir, kF16, 1>(a, (unsigned)tiles, s);
-    return launch_parts<kDir, kF16, 0>(a, (unsigned)tiles, s);
+        return launch_parts<kDir, kF16, 1, 0>(a, (unsigned)tiles, s);
+    return launch_parts<kDir, kF16, 0, 0>(a, (unsigned)tiles, s);
+}
+
+// Weight gradients of few tiles and many rows (adapter factors): as many blocks as would be idle, up to eight, share a
+// tile's rows, at least 128 rows of the average group each (4000 rows, 3 experts of 51 x 75: 15.7 us, one block a tile 75;
+// 1200 rows of 500 x 333: 13.6 and 54).
+int dw_splits(const GmmArgs& a) {
+    const int64_t tiles = (int64_t)a.G * ((a.N + kT - 1) / kT) * ((a.K + kT - 1) / kT);
+    int splits = 8;
+    while (splits > 1 && (tiles * splits > device_sms() || a.M / a.G < 128 * splits)) splits /= 2;
+    return splits;
 }
 
 }  // namespace
 
 cudaError_t launch_grouped(int dir, int f16, const GmmArgs& a, cudaStream_t s) {
     if (grouped_tc_supported(dir, a)) return launch_grouped_tc(dir, f16, a, 0, s);
-    switch (dir) {
-        case kGmmFwd: return f16 ? launch_any<kGmmFwd, 1>(a, s) : launch_any<kGmmFwd, 0>(a, s);
-        case kGmmDx: return f16 ? launch_any<kGmmDx, 1>(a, s) : launch_any<kGmmDx, 0>(a, s);
-        default: return f16 ? launch_any<kGmmDw, 1>(a, s) : launch_any<kGmmDw, 0>(a, s);
+    if (dir == kGmmDw) {
+        GmmArgs b = a;
+        b.splits = dw_splits(a);
+        return f16 ? launch_any<kGmmDw, 1>(b, s) : launch_any<kGmmDw, 0>(b, s);
     }
+    if (dir == kGmmFwd) return f16 ? launch_any<kGmmFwd, 1>(a, s) : launch_any<kGmmFwd, 0>(a, s);
+    return f16 ? launch_any<kGmmDx, 1>(a, s) : launch_any<kGmmDx, 0>(a, s);
 }
 
 }  // namespace moeq

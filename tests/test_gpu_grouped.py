@@ -345,3 +345,21 @@ def test_the_longest_sums_of_one_sign(kind, N, K):
     ref, mag, n = grouped_ref(kind, off, x, W, dy)
     step = torch.exp2(torch.floor(torch.log2(ref.clamp(min=2.0 ** -14)))) * 2.0 ** -10
     assert_within(out, ref, step / 2 + (sum_err(8192, 1) + 64 * 2.0 ** -24) * mag + 2.0 ** -25, "long sums")
+
+
+@pytest.mark.parametrize("sizes", [[5000], [2100, 0, 1, 4000], [1024, 1030], [300, 290]])
+@pytest.mark.parametrize("N,K", [(16, 264), (51, 75), (130, 8)])
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", "bf16"), ("fp16", "fp32"), ("bf16", "fp32")])
+def test_weight_gradients_of_few_tiles_and_many_rows(sizes, N, K, dtype, out_dtype):
+    """Blocks that share a tile's rows: rows before and behind the groups are NaN, accumulation adds once, and the
+    result is the same again."""
+    _check("dw", dtype, sizes, N, K, first=2, tail=3, out_dtype=out_dtype, seed=11)
+    x, dy, W, off, M = _case(12, sizes, N, K, dtype)
+    once, _ = _run("dw", dtype, x, dy, W, off, M, len(sizes), N, K, out_dtype)
+    old = torch.randn(once.shape, generator=torch.Generator(device="cuda").manual_seed(13), device="cuda").to(once.dtype)
+    outs = [_run("dw", dtype, x, dy, W, off, M, len(sizes), N, K, out_dtype, 1, old.clone())[0] for _ in range(2)]
+    assert torch.equal(*outs)
+    ref, mag, n = grouped_ref("dw", off, x=x, dy=dy)
+    ref += old.double()
+    tol = HALF[out_dtype] * ref.abs() + 1.01 * sum_err(min(n, 512) + n // 64, mag) + 2.0 ** -24 * (mag + old.double().abs())
+    assert_within(outs[0], ref, tol if out_dtype == "fp32" else tol + 1.01 * sum_err(n, mag), "added")
