@@ -20,8 +20,9 @@ struct GmmArgs {
     int M, G, N, K;
     int out_f32;         // dw: fp32 output instead of the inputs' type
     int accumulate;      // dw: out += instead of out =
-    // dw of unaligned rows: blocks that share a tile's rows; forward and dx of one group without offsets: the sum in `splits` parts of `per` terms (a multiple of 64), each
-    // written as fp32 [splits][M][outputs] to `partial` instead of `out`; splits <= 1: not split
+    // dw: blocks that share a tile's rows (the launchers set it); forward and dx of one group without offsets: the sum in
+    // `splits` parts of `per` terms (a multiple of 64), each written as fp32 [splits][M][outputs] to `partial` instead of
+    // `out`; splits <= 1: not split
     int splits, per;
     float* partial;
     int32_t* status;

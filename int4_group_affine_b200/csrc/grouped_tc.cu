@@ -15,6 +15,10 @@
 // 128-byte-swizzled boxes that TMA writes are the tensor core's own layout for either, so nothing is
 // transposed by hand.
 //
+// Weight gradients of few tiles and many rows: a cluster of up to eight blocks shares a tile's rows,
+// each leaves its sums in shared memory where the operands were, and each adds up its part of the
+// columns from all of them, in order.
+//
 // Forward and dx share a tile between a cluster's two blocks (cta_group::2): each loads its 128 lanes
 // and half of the columns, a third fewer bytes than two tiles of 128 x 256 take (7 % on 16 groups of
 // about 960 rows).  Matrices of 128 outputs or fewer, and dw, run on single blocks: in dw every tile
@@ -195,6 +199,7 @@ struct Schedule {
     bool good;
     int g = -1, across, left;              // left: tiles (forward, dx: of this group) from this one on
     int within, step, step_g;              // dw: tile within the group, and the stride in groups and tiles
+    int share, shares;                     // dw: of a tile's rows this block sums up share / shares
     int parts, width;                      // forward, dx: tiles along the group's rows, and their width
     int64_t tile;
     int total;                             // with a table: all tiles
@@ -211,6 +216,7 @@ struct Schedule {
             const Quot q = quot(first, left, inv_real), s = quot(stride, left, inv_real);
             g = q.q, within = q.r;
             step_g = s.q, step = s.r;
+            share = 0, shares = 1;
             fetch(p.a, lane);
         } else {
             total = table ? table->total : 0;
@@ -241,6 +247,11 @@ struct Schedule {
             t.terms = rows.end - rows.begin;
             t.first = t.part = 0;
             t.row0 = rows.begin;
+            if (shares > 1) {
+                const int per = ((t.terms + kStep - 1) / kStep + shares - 1) / shares * kStep;
+                t.row0 += min(share * per, t.terms);
+                t.terms = min(max(t.terms - share * per, 0), per);
+            }
             within += step;
             int ng = g + step_g;
             if (within >= left) within -= left, ++ng;
@@ -353,6 +364,15 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+// A float of the cluster's block `rank`, at this block's shared memory address `addr`.
+__device__ __forceinline__ float ld_of(uint32_t addr, int rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 template <int kCta>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {  // a warp of every block of the tile
@@ -510,7 +530,8 @@ struct Place {
     }
 };
 
-template <int kDir, int kF16, int kCta, int kNarrow>
+// kSplit: the a.splits blocks of a cluster share the rows of a tile (weight gradients; one tile a cluster).
+template <int kDir, int kF16, int kCta, int kNarrow, int kSplit>
 __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_constant__ TcGmm p) {
     using R = Ring<kDir, kCta, kNarrow>;
     constexpr int kStages = R::stages, kStageBytes = R::bytes, kTerms = kStep * R::steps;  // terms of a stage
@@ -565,7 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
     const uint32_t tmem = s_tmem;
     const uint32_t sbase = tc::smem_u32(sm);
     Schedule<kDir, kCta> sched;
-    sched.start(p, blockIdx.x / kCta, gridDim.x / kCta, lane, good, kDir != kGmmDw && p.table && good ? &s_table : nullptr);
+    const int team = kSplit ? a.splits : kCta;  // blocks of a tile
+    sched.start(p, blockIdx.x / team, gridDim.x / team, lane, good, kDir != kGmmDw && p.table && good ? &s_table : nullptr);
+    if (kSplit) sched.share = blockIdx.x % team, sched.shares = team;
     const int part = kDir == kGmmDw && a.out_f32 ? kPart : kPart16;  // long sums in parts
 
     if (warp == 0) {
@@ -712,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
             int p0 = t.first;
-            if (kDir != kGmmDw || !a.out_f32)
+            if (kDir != kGmmDw || kSplit || !a.out_f32)
                 for (; ok && t.terms - p0 > part; p0 += part, ++acc) {
                     ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
                     if (!ok) break;
@@ -782,6 +805,30 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             const int n0 = t.lane0 + kLanes * rank + 32 * q, n = n0 + lane;
             const int per = a.out_f32 ? 32 : 64;
             const bool empty = t.terms == 0;
+            if (kSplit) {  // this block's sums, to where the operands were: [column][row of the tile]
+                if (!empty) {
+                    ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                }
+                for (int c0 = kBand * half; c0 < t.cols; c0 += 2 * kBand)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float* to = reinterpret_cast<float*>(sm) + (c0 + 32 * h) * kLanes + 32 * q + lane;
+                        uint32_t v[32];
+                        if (!empty) {
+                            tmem_ld32(own + (acc & 1) * kCols + c0 + 32 * h, v);
+                            tc::tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float f = empty ? 0.0f : __uint_as_float(v[j]);
+                            if (p0 > 0) f += sum[c0 / 128 * 64 + 32 * h + j];
+                            to[j * kLanes] = f;
+                        }
+                    }
+                break;
+            }
             if (empty && a.accumulate) continue;
             while (ok && (p0 < t.terms || empty)) {
                 const bool add = a.accumulate || (a.out_f32 && p0 > 0);
@@ -858,6 +905,44 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         if (kDir == kGmmDw) bulk_wait();  // the last boxes are read (and written) before the block ends
     }
     __syncwarp();
+    if constexpr (kSplit) {
+        // Every block adds up its share of the columns, in the blocks' order: eight columns of a row a thread and step.
+        cluster_arrive();
+        cluster_wait();
+        const int tile = blockIdx.x / team, g = tile / p.real, in = tile % p.real;
+        const int n = in / p.across * kLanes + tid % kLanes, col0 = in % p.across * kCols, share = kCols / team;
+        const int c1 = min((sched.share + 1) * share, a.K - col0);
+        if (tid < 2 * kLanes && n < a.N)
+            for (int c = sched.share * share + tid / kLanes * 8; c < c1; c += 16) {
+                float f[8] = {};
+                for (int b = 0; b < team; ++b)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] += ld_of(sbase + ((c + j) * kLanes + tid % kLanes) * 4, b);
+                const int64_t at = ((int64_t)g * a.N + n) * a.K + col0 + c;
+                if (a.out_f32) {
+                    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 old = a.accumulate ? o[h] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        o[h] = make_float4(old.x + f[4 * h], old.y + f[4 * h + 1], old.z + f[4 * h + 2], old.w + f[4 * h + 3]);
+                    }
+                } else {
+                    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
+                    if (a.accumulate) {
+                        const uint4 old = *o;
+                        const uint32_t e[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] += from16<kF16>((uint16_t)(e[j / 2] >> (j % 2 * 16)));
+                    }
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = pack16<kF16>(__float_as_uint(f[2 * j]), __float_as_uint(f[2 * j + 1]));
+                    *o = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        __syncwarp();
+        cluster_arrive_relaxed(), cluster_wait();  // (no block ends while another reads it)
+    }
     if (kCta == 2) cluster_arrive_relaxed(), cluster_wait();  // (neither block ends while the other still reaches into it)
     else __syncthreads();
     if (warp == 1) tmem_free<kCta>(tmem, 512);
@@ -902,13 +987,16 @@ bool encode_mn(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kDir, int kF16, int kCta, int kNarrow>
+template <int kDir, int kF16, int kCta, int kNarrow, int kSplit = 0>
 cudaError_t launch_cta(const TcGmm& p, int64_t tiles, cudaStream_t s) {
     constexpr size_t smem = Ring<kDir, kCta, kNarrow>::smem;
-    constexpr auto kernel = gmm_tc_kernel<kDir, kF16, kCta, kNarrow>;
+    constexpr auto kernel = gmm_tc_kernel<kDir, kF16, kCta, kNarrow, kSplit>;
+    using R = Ring<kDir, kCta, kNarrow>;
+    static_assert(!kSplit || (kDir == kGmmDw && kCols * kLanes * 4 <= R::stages * R::bytes), "sums take the operands' place");
     static SmemLimit limit;
     const cudaError_t e = limit.raise((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
+    if (kSplit) return launch_dependent(kernel, dim3((unsigned)tiles * p.a.splits), kThreads, smem, p.a.splits, s, p);
     return launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(tiles, device_sms() / kCta) * kCta), kThreads, smem,
                             kCta, s, p);
 }
@@ -918,6 +1006,8 @@ cudaError_t launch_dir(const TcGmm& p, int pair, int64_t tiles, cudaStream_t s) 
     if constexpr (kDir != kGmmDw)
         if (pair)
             return p.a.M <= kNarrowRows ? launch_cta<kDir, kF16, 2, 1>(p, tiles, s) : launch_cta<kDir, kF16, 2, 0>(p, tiles, s);
+    if constexpr (kDir == kGmmDw)
+        if (p.a.splits > 1) return launch_cta<kDir, kF16, 1, 0, 1>(p, tiles, s);
     return launch_cta<kDir, kF16, 1, 0>(p, tiles, s);
 }
 
@@ -957,6 +1047,12 @@ cudaError_t launch_grouped_tc(int dir, int f16, const GmmArgs& a, int pitch, cud
         p.across = (a.K + kCols - 1) / kCols;
         p.real = (int)tiles * p.across;
         tiles = (int64_t)a.G * p.real;
+        // Few tiles and many rows (adapter factors): as many blocks as would be idle, up to eight, share a tile's rows, at
+        // least two steps of the average group's each (16384 rows, one group, 16 x 2048, fp32: 27 us, one block a tile 91;
+        // 6712 rows, 3 groups of 64 x 88: 8.5 and 19.7; 1024 rows, 16 x 2048: 9.5 and 9.9).
+        int splits = 8;
+        while (splits > 1 && (tiles * splits > device_sms() || a.M / a.G < 2 * kStep * splits)) splits /= 2;
+        p.a.splits = splits;
     } else {
         const int64_t terms = pitch ? pitch : dir == kGmmFwd ? a.K : a.N;
         ok = p.wide_a ? encode_mn(&p.tma, t, a.b, a.K, a.N, a.G, 2)
