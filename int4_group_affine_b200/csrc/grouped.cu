@@ -13,9 +13,10 @@
 // is kept [row][term], one whose rows are, [term][row], which ldmatrix transposes; pitches of 80 and
 // 272 bytes put the eight rows of an ldmatrix in different banks.
 //
-// Bound by the instructions that shift and place the operands and by the warp-level tensor path (about
-// a quarter of tcgen05's rate): 8000 rows on experts of 1003 to 1001, forward 141 us (114 TFLOP/s; with
-// 2-byte loads into 64 x 64 tiles 369), weight gradient 156.
+// Bound by the instructions that fetch, shift and place the operands (a step of a lone block takes 2500
+// cycles: copies 500 to 800, shifting 1000 to 1400, products 800) and by the warp-level tensor path
+// (about a quarter of tcgen05's rate): 8000 rows on experts of 1003 to 1001, forward 144 us (112 TFLOP/s;
+// with 2-byte loads into 64 x 64 tiles 369), weight gradient 137, to fp32 160.
 #include <cuda_fp16.h>
 
 #include "grouped.cuh"
@@ -71,6 +72,13 @@ __device__ __forceinline__ float from16(uint16_t v) {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // (the rest of the 16: zeros)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// 16 whole bytes where `on`, without a branch.
+__device__ __forceinline__ void cp16_if(uint32_t dst, const void* src, uint32_t on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+                 "l"(src), "r"(on)
+                 : "memory");
 }
 
 // Eight 16-bit elements out of the two aligned pieces they lie in, from byte `off` on; the first n count.
@@ -132,19 +140,26 @@ struct Operand {
     // step's are all inside the tensor.
     static constexpr int kCopies = (kLines * kPieces + kThreads - 1) / kThreads, kPlaces = kLines * kEights / kThreads;
     const char* src[kCopies];
-    bool safe[kCopies];
+    uint32_t safe;  // bit h: piece h of every whole step is inside the tensor
+    bool easy;      // every piece of the warp is that, or of a dead line
     int off[kPlaces], count[kPlaces];
 
     __device__ __forceinline__ void start(int tid) {
         const int64_t steps = terms / kKT;  // whole ones
+        bool edge = false;
+        safe = 0;
 #pragma unroll
         for (int h = 0; h < kCopies; ++h) {
             const int i = tid + h * kThreads, l = min(i / kPieces, kLines - 1);
             src[h] = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(line(0, l)) & ~(uintptr_t)15) + i % kPieces * 16;
-            safe[h] = i < kLines * kPieces && steps > 0 && (kRows || live(0, l)) &&
-                      src[h] >= reinterpret_cast<const char*>(first) &&
-                      src[h] + (steps - 1) * (kRows ? ld * (2 * kKT) : 2 * kKT) + 16 <= reinterpret_cast<const char*>(last);
+            if (i >= kLines * kPieces || steps == 0 || !(kRows || live(0, l))) continue;
+            if (src[h] >= reinterpret_cast<const char*>(first) &&
+                src[h] + (steps - 1) * (kRows ? ld * (2 * kKT) : 2 * kKT) + 16 <= reinterpret_cast<const char*>(last))
+                safe |= 1u << h;
+            else
+                edge = true;
         }
+        easy = !__any_sync(0xffffffffu, edge);
 #pragma unroll
         for (int h = 0; h < kPlaces; ++h) {
             const int i = tid + h * kThreads, l = i / kEights;
@@ -155,9 +170,17 @@ struct Operand {
     __device__ __forceinline__ void copy(unsigned char* raw, int t0, int tid) {
         const bool whole = t0 + kKT <= terms;
         const uint32_t dst0 = (uint32_t)__cvta_generic_to_shared(raw) + tid * 16;
+        if (whole && easy) {
+#pragma unroll
+            for (int h = 0; h < kCopies; ++h) {
+                cp16_if(dst0 + h * kThreads * 16, src[h], safe >> h & 1);
+                src[h] += kRows ? ld * (2 * kKT) : 2 * kKT;
+            }
+            return;
+        }
 #pragma unroll
         for (int h = 0; h < kCopies; ++h) {
-            if (whole && safe[h]) cp16(dst0 + h * kThreads * 16, src[h], 16);
+            if (whole && (safe >> h & 1)) cp16(dst0 + h * kThreads * 16, src[h], 16);
             else if (tid + h * kThreads < kLines * kPieces && live(t0, (tid + h * kThreads) / kPieces))
                 copy_edge(raw + (tid + h * kThreads) * 16, src[h], first, last);
             src[h] += kRows ? ld * (2 * kKT) : 2 * kKT;  // (32 rows are whole pieces whatever their length)
