@@ -472,7 +472,8 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  * `in`, packed words 16-byte aligned; out, in <= MOEQ_MAX_WIDTH or MOE_ERR_UNSUPPORTED (out: up to
  * 1 << 24), and T <= MOEQ_MAX_ROWS.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
  * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  With few rows (16, or a few times as many for
- * small matrices) the codes enter the sums as whole numbers, s and b once per group; larger T, and every
+ * small matrices) the codes enter the sums as whole numbers, s and b once per group, and x is exact down to 2^-27
+ * of the largest of its 32 or 64 neighbours, off by at most 2^-35 of that below; larger T, and every
  * dx, first writes the matrix into the workspace as bf16 (one rounding per weight, at most 2^-8 of it)
  * and multiplies that.  An infinite
  * or NaN input makes the outputs that depend on it infinite or NaN.
@@ -511,7 +512,7 @@ MOEQ_API moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* d
  * Any N and K up to MOEQ_MAX_WIDTH, M up to MOEQ_MAX_ROWS, G up to MOEQ_MAX_GROUPS (MOE_ERR_UNSUPPORTED beyond).  Operands that
  * start on 16 bytes and whose rows (x, dy, W; dw) are multiples of 16 bytes run on the tcgen05
  * kernel, others on warp-level tiles.  Results do not depend on the other groups' rows or, run to run, on
- * scheduling.  Outputs may not alias inputs.  M = 0 enqueues nothing but dw's zeros. */
+ * scheduling; the order in which a long sum's parts are added depends on the call's sizes alone.  Outputs may not alias inputs.  M = 0 enqueues nothing but dw's zeros. */
 MOEQ_API moe_status moe_grouped_matmul(int32_t dtype, const void* x, const int32_t* offsets, const void* W, int32_t M,
                                        int32_t G, int32_t N, int32_t K, void* y, int32_t* status, moe_stream stream);
 MOEQ_API moe_status moe_grouped_matmul_dx(int32_t dtype, const void* dy, const int32_t* offsets, const void* W,
