@@ -469,8 +469,8 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  *  moe_affine_linear_dx: dx[t][k] = sum_n dy[t][n] (s q + b)[n][k], the gradient of x through
  *    the frozen packed weights (adapter training over the int4 base, section 二 of that page).
  * W: one matrix (n = 1) of either affine format, any `out`, group a multiple of 32 that divides
- * `in`, packed words 16-byte aligned; out, in <= MOEQ_MAX_WIDTH or MOE_ERR_UNSUPPORTED (out: up to
- * 1 << 24), and T <= MOEQ_MAX_ROWS.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
+ * `in`, packed words 16-byte aligned; in <= MOEQ_MAX_WIDTH, out <= 1 << 24 and T <= MOEQ_MAX_ROWS, or
+ * MOE_ERR_UNSUPPORTED.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
  * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  With few rows (16, or a few times as many for
  * small matrices) the codes enter the sums as whole numbers, s and b once per group, and x is exact down to 2^-27
  * of the largest of its 32 or 64 neighbours, off by at most 2^-35 of that below; larger T, and every
