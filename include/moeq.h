@@ -478,8 +478,8 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  * and multiplies that.  An infinite
  * or NaN input makes the outputs that depend on it infinite or NaN.
  * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses),
- * 256-byte aligned, initialised once with moe_workspace_init; it holds the status word, and
- * nothing else outlives a call, but calls that may run at the same time (two streams, two graphs'
+ * 256-byte aligned, initialised once with moe_workspace_init (bytes that never fall with T: one for the
+ * largest T serves fewer rows); it holds the status word, and nothing else outlives a call, but calls that may run at the same time (two streams, two graphs'
  * replays) each need their own.  T = 0 enqueues nothing. */
 MOEQ_API size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T);
 MOEQ_API moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y,

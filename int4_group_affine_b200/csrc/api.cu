@@ -1004,9 +1004,15 @@ moe_status linear_product(const moe_qtensor* W, bool dx, const uint16_t* rows, i
 }
 }  // namespace
 
+// The choice can go back from the matrix to the codes as T grows (more tiles end the split of a long sum), and a workspace
+// for T rows serves fewer: where T takes the codes, fewer rows that take the matrix count.  Among 256 rows that share
+// their tiles the matrix costs the same and the codes more with every row, so the last of them tells.
 size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T) {
     if (T < 0 || T > MOEQ_MAX_ROWS || linear_check(W) != MOE_OK) return 0;
-    return T > 0 && linear_matrix(W, T) ? linear_plan(W, T, false).total : kAlign;
+    if (T > 0 && linear_matrix(W, T)) return linear_plan(W, T, false).total;
+    for (int t = (T - 1) / 256 * 256; t > 0; t -= 256)
+        if (linear_matrix(W, t)) return linear_plan(W, t, false).total;
+    return kAlign;
 }
 
 moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y, void* workspace,
@@ -1015,13 +1021,14 @@ moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T,
     if (st != MOE_OK) return st;
     CHECK_ARG(T >= 0);
     if (T > MOEQ_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
-    st = ws_check(workspace, ws_bytes, moe_affine_linear_workspace_bytes(W, T));
+    const bool matrix = T > 0 && linear_matrix(W, T);
+    st = ws_check(workspace, ws_bytes, matrix ? linear_plan(W, T, false).total : kAlign);
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
     CHECK_ARG(x && y && x != y && aligned(x, 16) && aligned(y, 2));
     cudaStream_t s = (cudaStream_t)stream;
     timing_begin(s);
-    if (linear_matrix(W, T)) return linear_product(W, false, x, T, y, workspace, s);
+    if (matrix) return linear_product(W, false, x, T, y, workspace, s);
     LAUNCH(kAffineLinear, launch_affine_linear(*W, x, T, y, s));
     return MOE_OK;
 }
