@@ -423,6 +423,14 @@ __device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
             "r"(one), "h"((uint16_t)3)
             : "memory");
 }
+// The same on a barrier of this block alone.
+template <int kCta>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+    if (kCta == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 __device__ __forceinline__ void tma_store_3d(uint32_t one, const void* map, uint32_t src, int x, int y, int z) {
     asm volatile(
@@ -520,6 +528,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 
 // The bound of a block's last waits: what is under way ends by itself, also where the waits before were cut short.
 __device__ __forceinline__ uint64_t drain_ns(const GmmArgs& a) { return a.wait_ns > 1000000000ull ? a.wait_ns : 1000000000ull; }
+
+// A millisecond, for what is under way and cannot be waited for after the blocks have given up.
+__device__ __forceinline__ void let_pass() {
+    for (const uint64_t t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 1000000;) {
+    }
+}
 
 // A place in the ring of stages, and the parity its barriers complete with next.
 template <int kStages>
@@ -645,14 +659,18 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 }
             }
         }
-        // No block ends with copies on their way into it, however the others fared.  (A pair's copies report to its
-        // first block; should the two have parted in giving up, the second cannot tell and lets time pass.)
-        if (one && rank == 0) {
-            for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-                tc::mbar_wait(&bar_full[i % kStages], (i / kStages) & 1, a.status, drain_ns(a));
-        } else if (one && !(ok && s_ok)) {
-            for (const uint64_t t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 1000000;) {
-            }
+        // No block ends with copies on their way into it, or the tensor core's reports that a stage was multiplied, which
+        // a pair's first block sends to both.  (A pair's copies report to its first block, and a stage that was multiplied
+        // had landed; should the two have parted in giving up, what is left cannot be told and gets time to pass.)
+        if (one) {
+            const uint32_t last = n > kStages ? n - kStages : 0;
+            if (rank == 0)
+                for (uint32_t i = last; i < n; ++i)
+                    tc::mbar_wait(&bar_full[i % kStages], (i / kStages) & 1, a.status, drain_ns(a));
+            bool all = ok;
+            for (uint32_t i = last; all && i < n; ++i)
+                all = tc::mbar_wait_ok(&bar_empty[i % kStages], (i / kStages) & 1, a.status, &s_ok, drain_ns(a));
+            if (!all) let_pass();
         }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ products
@@ -710,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             }
         }
         if (one) {  // and none with products under way
-            commit<kCta>(1, tc::smem_u32(&bar_drain));
+            commit_here<kCta>(tc::smem_u32(&bar_drain));
             tc::mbar_wait(&bar_drain, 0, a.status, drain_ns(a));
         }
     } else if (warp > 1) {
