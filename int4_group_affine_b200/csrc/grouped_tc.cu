@@ -727,7 +727,13 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 p0 = p1;
             }
         }
-        if (one) {  // and none with products under way
+        // and none with products under way, or the second block's reports that it has read an accumulator
+        if (kCta == 2) {
+            bool all = ok;
+            for (uint32_t i = acc > 2 ? acc - 2 : 0; all && i < acc; ++i) all = warp_wait(&bar_free[i & 1], i / 2 & 1, a, &s_ok);
+            if (one && !all) let_pass();
+        }
+        if (one) {
             commit_here<kCta>(tc::smem_u32(&bar_drain));
             tc::mbar_wait(&bar_drain, 0, a.status, drain_ns(a));
         }
