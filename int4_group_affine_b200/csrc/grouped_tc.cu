@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                 }
             }
         __syncwarp();
-        cluster_arrive_relaxed(), cluster_wait();  // (no block ends while another reads it)
+        cluster_arrive(), cluster_wait();  // (no block ends while another reads it: the reads come before this arrival)
     }
     if (kCta == 2) cluster_arrive_relaxed(), cluster_wait();  // (neither block ends while the other still reaches into it)
     else __syncthreads();
