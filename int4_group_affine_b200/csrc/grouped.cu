@@ -115,7 +115,7 @@ __device__ __noinline__ void copy_edge(unsigned char* dst, const char* src, cons
         cp16((uint32_t)__cvta_generic_to_shared(dst), reinterpret_cast<const void*>(from), bytes);
     } else {  // the tensor begins inside the piece
         for (int b = (int)(begin - src); b < 16 && src + b < end; b += 2)
-            *reinterpret_cast<uint16_t*>(dst + b) = __ldg(reinterpret_cast<const uint16_t*>(src + b));
+            *reinterpret_cast<uint16_t*>(dst + b) = ld_after(reinterpret_cast<const uint16_t*>(src + b));
     }
 }
 

@@ -43,7 +43,7 @@ struct GmmRows {
     int begin, end;
 };
 
-__device__ __forceinline__ int gmm_clamped(const GmmArgs& a, int g) { return min(max(__ldg(a.off + g), 0), a.M); }
+__device__ __forceinline__ int gmm_clamped(const GmmArgs& a, int g) { return min(max(ld_after(a.off + g), 0), a.M); }
 
 // The rows of group g (a whole warp; the result is the same in every lane).
 __device__ __forceinline__ GmmRows gmm_rows_of(const GmmArgs& a, int g, int lane) {
@@ -120,8 +120,8 @@ __device__ __forceinline__ bool gmm_check_offsets(const GmmArgs& a, int tid, int
     if (!a.off) return true;
     bool good = true;
     for (int g = tid; g <= a.G; g += nthreads) {
-        const int v = __ldg(a.off + g);
-        if (v < 0 || v > a.M || (g > 0 && __ldg(a.off + g - 1) > v)) good = false;
+        const int v = ld_after(a.off + g);
+        if (v < 0 || v > a.M || (g > 0 && ld_after(a.off + g - 1) > v)) good = false;
     }
     if (!good && blockIdx.x == 0) raise_status(a.status, MOE_ERR_DEVICE_INDEX);
     return good;

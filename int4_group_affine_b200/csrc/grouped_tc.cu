@@ -131,7 +131,7 @@ struct Table {
 template <int kThreads>
 __device__ __forceinline__ bool fill_table(Table& tb, const GmmArgs& a, int across, int tid) {
     const int warp = tid / 32, lane = tid % 32, windows = (a.G + 31) / 32;
-    for (int i = tid; i <= a.G; i += kThreads) tb.off[i] = __ldg(a.off + i);
+    for (int i = tid; i <= a.G; i += kThreads) tb.off[i] = ld_after(a.off + i);
     __syncthreads();
     bool good = true;
     for (int i = tid; i <= a.G; i += kThreads) good = good && tb.off[i] >= (i > 0 ? tb.off[i - 1] : 0) && tb.off[i] <= a.M;
@@ -230,7 +230,7 @@ struct Schedule {
     __device__ __forceinline__ void fetch(const GmmArgs& a, int lane) {
         if (g >= a.G) return;
         if (!good) rows = gmm_rows_of(a, g, lane);
-        else rows = a.off ? GmmRows{__ldg(a.off + g), __ldg(a.off + g + 1)} : GmmRows{0, a.M};
+        else rows = a.off ? GmmRows{ld_after(a.off + g), ld_after(a.off + g + 1)} : GmmRows{0, a.M};
     }
 
     // The next tile; g = -1 when there is none.

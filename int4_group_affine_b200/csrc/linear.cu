@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
                     const uint32_t u = min(cq * kQuad + i, a.units - 1), gi = a.inv_span ? __umulhi(u, a.inv_span) : u;
 #pragma unroll
                     for (int m = 0; m < kMT; ++m)
-                        pend[m][i] = __ldg(sb + (int64_t)min(m * 16 + lane / 2, last) * groups + gi);
+                        pend[m][i] = ld_after(sb + (int64_t)min(m * 16 + lane / 2, last) * groups + gi);
                 }
             }
             if (++cq == q1) cq = q0, ctile += stride;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_codes_kernel(const LinArgs
         for (int h = 0; h < kAhead; ++h) {
             tt[h] = t, cc[h] = ch;
             v[h] = make_uint4(0, 0, 0, 0);
-            if (t < nt) v[h] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + t) * K) + ch);
+            if (t < nt) v[h] = ld_after(reinterpret_cast<const uint4*>(a.x + (int64_t)(t0 + t) * K) + ch);
             t += a.step_t, ch += a.step_c;
             if (ch >= chunks) ch -= chunks, ++t;
         }
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int
         const int c = (int)(i - t * pad.pitch8) * 8;
         uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < pad.n ? __ldg(pad.x + t * pad.n + c + j) : 0;
+        for (int j = 0; j < 8; ++j) v[j] = c + j < pad.n ? ld_after(pad.x + t * pad.n + c + j) : 0;
         pad.out[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
     for (int64_t i0 = (int64_t)blockIdx.x * (256 * kPieces) + threadIdx.x; i0 < pieces;
@@ -472,14 +472,14 @@ __global__ void __launch_bounds__(256) dequant16_kernel(const moe_qtensor W, int
             const int64_t i = i0 + j * 256;
             if (i >= pieces) break;
             if constexpr (kBits == 4) {
-                w[j][0] = __ldg(W.packed + i);
+                w[j][0] = ld_after(W.packed + i);
             } else {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(W.packed) + i);
+                const uint2 v = ld_after(reinterpret_cast<const uint2*>(W.packed) + i);
                 w[j][0] = v.x, w[j][1] = v.y;
             }
             const int64_t g = shift >= 0 ? i >> shift : i / groups8;  // (a row is a whole number of groups)
-            s[j] = __ldg(W.scales + g);
-            b[j] = __ldg(W.biases + g);
+            s[j] = ld_after(W.scales + g);
+            b[j] = ld_after(W.biases + g);
         }
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(256) add_parts_kernel(const float* __restrict_
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         float v = 0.0f;
 #pragma unroll 8
-        for (int s = 0; s < splits; ++s) v += __ldg(parts + s * n + i);
+        for (int s = 0; s < splits; ++s) v += ld_after(parts + s * n + i);
         y[i] = f2bf16(v);
     }
 }

@@ -25,7 +25,7 @@ struct Range {
 // (begin >= end: no rows)
 __device__ __forceinline__ Range rows_of(const SwigluArgs& a) {
     if (!a.off) return Range{0, a.M};
-    return Range{max(__ldg(a.off), 0), min(__ldg(a.off + a.G), a.M)};
+    return Range{max(ld_after(a.off), 0), min(ld_after(a.off + a.G), a.M)};
 }
 
 // sigmoid(g) without overflow: e = exp(-|g|) <= 1 and 1 + e in [1, 2].  As a power of two, whose argument is rounded:
@@ -81,13 +81,13 @@ __global__ void __launch_bounds__(256) swiglu_vec_kernel(const SwigluArgs a) {
          m += (int64_t)gridDim.x * (256 / kTeam)) {
         const uint4 *gr = reinterpret_cast<const uint4*>(a.gu + m * 2 * a.I), *ur = gr + I8;
         const uint4* dr = reinterpret_cast<const uint4*>(a.dh + m * a.I);
-        const float w = a.w ? __ldg(a.w + m) : 1.0f;
+        const float w = a.w ? ld_after(a.w + m) : 1.0f;
         float dw = 0.0f;
 #pragma unroll 2
         for (int i = at; i < I8; i += kTeam) {
-            const uint4 g = __ldcs(gr + i), u = __ldcs(ur + i);
+            const uint4 g = ld_after_once(gr + i), u = ld_after_once(ur + i);
             uint4 d = make_uint4(0, 0, 0, 0);
-            if (kGrad) d = __ldcs(dr + i);
+            if (kGrad) d = ld_after_once(dr + i);
             float o1[8], o2[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -132,11 +132,12 @@ __global__ void __launch_bounds__(256) swiglu_any_kernel(const SwigluArgs a) {
     if (m < r.begin || m >= r.end) return;
     const int I = a.I;
     const uint16_t *gr = a.gu + m * 2 * I, *ur = gr + I;
-    const float w = a.w ? __ldg(a.w + m) : 1.0f;
+    const float w = a.w ? ld_after(a.w + m) : 1.0f;
     float dw = 0.0f;
+#pragma unroll 4
     for (int i = threadIdx.x; i < I; i += 256) {
-        const float d = kGrad ? ld16<kF16>(__ldg(a.dh + m * I + i)) : 0.0f;
-        const Elem e = element<kGrad>(ld16<kF16>(__ldg(gr + i)), ld16<kF16>(__ldg(ur + i)), w, d);
+        const float d = kGrad ? ld16<kF16>(ld_after(a.dh + m * I + i)) : 0.0f;
+        const Elem e = element<kGrad>(ld16<kF16>(ld_after(gr + i)), ld16<kF16>(ld_after(ur + i)), w, d);
         if (!kGrad) {
             a.h[m * I + i] = st16<kF16>(e.h);
         } else {
