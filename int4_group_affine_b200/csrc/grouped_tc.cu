@@ -46,8 +46,9 @@
 // Long sums: the tensor core's accumulation rounds toward zero, an error that grows with the sum's
 // length (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192; 4.5e-4 at 65536 of one sign, as
 // much as a rounding to fp16).  Sums of fp32 weight gradients longer than 512 rows leave the tensor
-// core in parts and are added by the L2's fp32 additions, one part after the other (a fixed order);
-// those for 16-bit results leave it every 8192 terms and are added up in fp32 by the result warps.
+// core in parts and are added by the L2's fp32 additions, one part after the other (a fixed order), or
+// by the result warps where an earlier gradient is to meet the complete sum; those for 16-bit results
+// leave it every 8192 terms and are added up in fp32 by the result warps.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
@@ -751,22 +752,26 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
         const int J = kDir == kGmmFwd ? a.N : a.K;
         const bool pairs = J % 2 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
         const uint32_t own = tmem + ((uint32_t)(32 * q) << 16);  // this warp's lanes
-        // Parts of a long sum before its last are added up here, kBand columns of every other band (in local memory:
-        // few sums are so long).
+        // Parts of a long sum before its last are added up here, `band` columns of every other band, those of the pieces
+        // that the warp writes (in local memory: few sums are so long).  fp32 weight gradients that nothing is added to
+        // leave their parts to the L2's additions (20000 rows, 2048 x 2048: 229 us, added up here 252; 200 groups of 700
+        // rows, 64 x 64: 13.1 and 14.0).
         constexpr int kBand = kDir == kGmmDw ? 64 : 32;
+        const bool fp32 = kDir == kGmmDw && !kSplit && a.out_f32, in_memory = fp32 && !a.accumulate;
+        const int band = fp32 ? 32 : kBand;
         float sum[kCols / 2];
         while (ok) {
             const Tile t = sched.next(a, lane);
             if (t.g < 0) break;
             int p0 = t.first;
-            if (kDir != kGmmDw || kSplit || !a.out_f32)
+            if (!in_memory)
                 for (; ok && t.terms - p0 > part; p0 += part, ++acc) {
                     ok = warp_wait(&bar_acc[acc & 1], (acc / 2) & 1, a, &s_ok);
                     if (!ok) break;
                     tc::tc_fence_after();
                     float* to = sum;
-                    for (int c0 = kBand * half; c0 < t.cols; c0 += 2 * kBand)
-                        for (int c = c0; c < c0 + kBand; c += 32, to += 32) {
+                    for (int c0 = band * half; c0 < t.cols; c0 += 2 * band)
+                        for (int c = c0; c < c0 + band; c += 32, to += 32) {
                             uint32_t v[32];
                             tmem_ld32(own + (acc & 1) * kCols + c, v);
                             tc::tmem_wait_ld();
@@ -855,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
             }
             if (empty && a.accumulate) continue;
             while (ok && (p0 < t.terms || empty)) {
-                const bool add = a.accumulate || (a.out_f32 && p0 > 0);
+                const bool later = in_memory && p0 > 0, add = a.accumulate || later;  // (a part behind the first)
                 const uint32_t buf = acc & 1;
                 if (!empty) {
                     ok = warp_wait(&bar_acc[buf], (acc / 2) & 1, a, &s_ok);
@@ -870,6 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                     } else if (a.out_f32) {
                         tmem_ld32(own + buf * kCols + c, w);
                         tc::tmem_wait_ld();
+                        if (p0 > 0 && !later)
+                            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + sum[c / 64 * 32 + j]);
                     } else {
                         uint32_t vv[2][32];
                         tmem_ld32(own + buf * kCols + c, vv[0]);
@@ -903,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm_tc_kernel(const __grid_consta
                         }
                     }
                     // the staging box is free, and earlier parts are in place
-                    if (p0 > 0) bulk_wait();
+                    if (later) bulk_wait();
                     else bulk_wait_read();
                     __syncwarp();
 #pragma unroll

@@ -126,3 +126,23 @@ def test_long_groups_of_one_sign(dtype, out_dtype, shape):
     tol = sum_err(min(n, 512 if out_dtype == "fp32" else 8192), mag) + 40 * 2.0 ** -24 * mag
     assert_within(got, ref, tol + HALF[out_dtype] * (ref + tol) + (2.0 ** -25 if out_dtype == "fp16" else 0))
     assert torch.equal(got, _call("dw", dtype, off, M, N, K, x, None, dy, out_dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("shape", LONG + [([5000], 16, 264), ([3000, 2000], 51, 75)], ids=_ids)
+def test_gradients_are_added_once(dtype, shape):
+    """accumulate in fp32: the sum of the rows is complete before it meets the earlier gradient, which is 1000 times as large
+    as a part of the sum: one rounding of the new value, half a step, whatever the number of parts; beside it the sum's own
+    error.  (Part by part onto it, 3000 rows and more are several steps off.)"""
+    sizes, N, K = shape
+    g = torch.Generator(device="cuda").manual_seed(K)
+    off = offsets_of(sizes, 0)
+    M = int(off[-1])
+    mk = lambda n: (0.005 + 0.01 * torch.rand((M, n), generator=g, device="cuda")).to(DTYPES[dtype])  # noqa: E731
+    x, dy = mk(K), mk(N)
+    old = 1000 + 16 * torch.rand((len(sizes), N, K), generator=g, device="cuda")
+    ref, mag, n = grouped_ref("dw", off, x=x, dy=dy)
+    want = ref + old.double()
+    got = _call("dw", dtype, off, M, N, K, x, None, dy, "fp32", old)
+    tol = sum_err(min(n, 512), mag) + 40 * 2.0 ** -24 * mag
+    assert_within(got, want, 2.0 ** -15 + tol)  # (a step of [512, 1024) is 2^-14)
