@@ -45,19 +45,16 @@ def _check(name, st):
         raise MoeError(name, st)
 
 
-_torch = None
-
-
-def _load_torch():
-    global _torch
-    import torch
-    torch.cuda.init()
-    _torch = torch
-    return torch
+_raw_stream = None
 
 
 def _device():
-    return (_torch or _load_torch())._C._cuda_getDevice()
+    """The current device (and from the first call on torch's own function for it, without the way through its modules)."""
+    global _device, _raw_stream
+    import torch
+    torch.cuda.init()
+    _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _device()
 
 
 def _ptr(t):
@@ -75,8 +72,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         # the handle of torch.cuda.current_stream() without building the Stream object (3 us a call)
-        c = (_torch or _load_torch())._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+        d = _device()
+        return _raw_stream(d)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -334,6 +331,38 @@ def _here(*tensors):
     return out
 
 
+_TYPES = None
+
+
+def _types():
+    """The types that a type code stands for: the type itself, or its bits."""
+    global _TYPES
+    import torch
+    bits = (torch.int16, torch.uint16)
+    _TYPES = {DT_BF16: (torch.bfloat16, *bits), DT_F16: (torch.float16, *bits), DT_F32: (torch.float32,),
+              _I32: (torch.int32,)}
+    return _TYPES
+
+
+_I32 = "int32"
+
+
+def _holds(t, need):
+    if t.__class__ is not int and t is not None and t.nbytes < need:
+        raise ValueError("a tensor has %d bytes, the call takes %d" % (t.nbytes, need))
+
+
+def _sizes(code, *args):
+    """Checks (tensor, the bytes of it that the call takes) of one type code: the library knows sizes and types by the
+    call's arguments alone, and a tensor that is shorter or of another type would be read or written beyond its end, or as
+    what it is not.  (Addresses go unchecked, and a code that is none is left for the library to refuse.)"""
+    types = (_TYPES or _types()).get(code)
+    for t, need in args:
+        if t.__class__ is not int and t is not None and (t.nbytes < need or types and t.dtype not in types):
+            _holds(t, need)
+            raise ValueError("a tensor is %s, the call takes %s" % (t.dtype, types[0]))
+
+
 def moe_affine_linear_workspace_bytes(W: QTensor, T) -> int:
     return int(_lib.lib().moe_affine_linear_workspace_bytes(ctypes.byref(W), T))
 
@@ -341,8 +370,9 @@ def moe_affine_linear_workspace_bytes(W: QTensor, T) -> int:
 def moe_affine_linear(W: QTensor, x, T, y, workspace, ws_bytes, stream=None):
     """y = x times the packed matrix (bf16 rows [T, in] -> [T, out])."""
     px, py, pw = _here(x, y, workspace)
-    _check("moe_affine_linear", _lib.lib().moe_affine_linear(ctypes.byref(W), px, T, py, pw, ws_bytes,
-                                                             _stream(stream)))
+    _sizes(DT_BF16, (x, 2 * T * W.in_), (y, 2 * T * W.out))
+    _holds(workspace, ws_bytes)
+    _check("moe_affine_linear", _lib.lib().moe_affine_linear(W, px, T, py, pw, ws_bytes, _stream(stream)))
 
 
 def moe_affine_linear_dx_workspace_bytes(W: QTensor, T) -> int:
@@ -352,13 +382,16 @@ def moe_affine_linear_dx_workspace_bytes(W: QTensor, T) -> int:
 def moe_affine_linear_dx(W: QTensor, dy, T, dx, workspace, ws_bytes, stream=None):
     """dx, the gradient of moe_affine_linear's x for the gradient dy of its y."""
     py, px, pw = _here(dy, dx, workspace)
-    _check("moe_affine_linear_dx", _lib.lib().moe_affine_linear_dx(ctypes.byref(W), py, T, px, pw, ws_bytes,
-                                                                   _stream(stream)))
+    _sizes(DT_BF16, (dy, 2 * T * W.out), (dx, 2 * T * W.in_))
+    _holds(workspace, ws_bytes)
+    _check("moe_affine_linear_dx", _lib.lib().moe_affine_linear_dx(W, py, T, px, pw, ws_bytes, _stream(stream)))
 
 
 def moe_grouped_matmul(dtype, x, offsets, W, M, G, N, K, y, status, stream=None):
     """y[m] = W[g] x[m] for the rows of each group g (dtype DT_BF16 or DT_F16)."""
     px, po, pw, py, ps = _here(x, offsets, W, y, status)
+    _sizes(dtype, (x, 2 * M * K), (W, 2 * G * N * K), (y, 2 * M * N))
+    _sizes(_I32, (offsets, 4 * G + 4), (status, 4))
     _check("moe_grouped_matmul", _lib.lib().moe_grouped_matmul(dtype, px, po, pw, M, G, N, K, py, ps,
                                                                _stream(stream)))
 
@@ -366,6 +399,8 @@ def moe_grouped_matmul(dtype, x, offsets, W, M, G, N, K, y, status, stream=None)
 def moe_grouped_matmul_dx(dtype, dy, offsets, W, M, G, N, K, dx, status, stream=None):
     """dx[m] = W[g]^T dy[m], the gradient of moe_grouped_matmul's x."""
     py, po, pw, px, ps = _here(dy, offsets, W, dx, status)
+    _sizes(dtype, (dy, 2 * M * N), (W, 2 * G * N * K), (dx, 2 * M * K))
+    _sizes(_I32, (offsets, 4 * G + 4), (status, 4))
     _check("moe_grouped_matmul_dx", _lib.lib().moe_grouped_matmul_dx(dtype, py, po, pw, M, G, N, K, px, ps,
                                                                      _stream(stream)))
 
@@ -373,6 +408,9 @@ def moe_grouped_matmul_dx(dtype, dy, offsets, W, M, G, N, K, dx, status, stream=
 def moe_grouped_matmul_dw(dtype, dy, x, offsets, M, G, N, K, out_dtype, accumulate, dw, status, stream=None):
     """dw[g] (+)= sum over the rows of group g of dy[m] x[m]^T, the gradient of moe_grouped_matmul's W."""
     py, px, po, pw, ps = _here(dy, x, offsets, dw, status)
+    _sizes(dtype, (dy, 2 * M * N), (x, 2 * M * K))
+    _sizes(out_dtype, (dw, (4 if out_dtype == DT_F32 else 2) * G * N * K))
+    _sizes(_I32, (offsets, 4 * G + 4), (status, 4))
     _check("moe_grouped_matmul_dw", _lib.lib().moe_grouped_matmul_dw(
         dtype, py, px, po, M, G, N, K, out_dtype, int(accumulate), pw, ps, _stream(stream)))
 
@@ -380,10 +418,16 @@ def moe_grouped_matmul_dw(dtype, dy, x, offsets, M, G, N, K, out_dtype, accumula
 def moe_swiglu(dtype, gu, w, offsets, G, M, I, h, stream=None):
     """h = w * silu(gate) * up of stacked rows gu = [gate | up] ([M, 2 I])."""
     pg, pw, po, ph = _here(gu, w, offsets, h)
+    _sizes(dtype, (gu, 4 * M * I), (h, 2 * M * I))
+    _sizes(DT_F32, (w, 4 * M))
+    _sizes(_I32, (offsets, 4 * G + 4))
     _check("moe_swiglu", _lib.lib().moe_swiglu(dtype, pg, pw, po, G, M, I, ph, _stream(stream)))
 
 
 def moe_swiglu_grad(dtype, gu, w, dh, offsets, G, M, I, dgu, dw, stream=None):
     """The gradients of moe_swiglu's gu and w (dw None: not wanted) for the gradient dh of its h."""
     pg, pw, pd, po, pu, px = _here(gu, w, dh, offsets, dgu, dw)
+    _sizes(dtype, (gu, 4 * M * I), (dh, 2 * M * I), (dgu, 4 * M * I))
+    _sizes(DT_F32, (w, 4 * M), (dw, 4 * M))
+    _sizes(_I32, (offsets, 4 * G + 4))
     _check("moe_swiglu_grad", _lib.lib().moe_swiglu_grad(dtype, pg, pw, pd, po, G, M, I, pu, px, _stream(stream)))
