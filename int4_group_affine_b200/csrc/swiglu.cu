@@ -122,7 +122,9 @@ __global__ void __launch_bounds__(256) swiglu_vec_kernel(const SwigluArgs a) {
     }
 }
 
-// Any size and alignment: one block per row.
+// Any size and alignment: one block per row, the loads of kAhead elements a thread under way together (16384 rows of 1001
+// 26.8 us, gradient 43.3; one by one, behind the ordered loads, 41.8 and 62.7).
+constexpr int kAhead = 4;
 template <int kF16, int kGrad>
 __global__ void __launch_bounds__(256) swiglu_any_kernel(const SwigluArgs a) {
     __shared__ float s_part[8];
@@ -131,19 +133,31 @@ __global__ void __launch_bounds__(256) swiglu_any_kernel(const SwigluArgs a) {
     const int64_t m = blockIdx.x;
     if (m < r.begin || m >= r.end) return;
     const int I = a.I;
-    const uint16_t *gr = a.gu + m * 2 * I, *ur = gr + I;
+    const uint16_t *gr = a.gu + m * 2 * I, *ur = gr + I, *dr = a.dh + m * I;
     const float w = a.w ? ld_after(a.w + m) : 1.0f;
     float dw = 0.0f;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < I; i += 256) {
-        const float d = kGrad ? ld16<kF16>(ld_after(a.dh + m * I + i)) : 0.0f;
-        const Elem e = element<kGrad>(ld16<kF16>(ld_after(gr + i)), ld16<kF16>(ld_after(ur + i)), w, d);
-        if (!kGrad) {
-            a.h[m * I + i] = st16<kF16>(e.h);
-        } else {
-            a.dgu[m * 2 * I + i] = st16<kF16>(e.dg);
-            a.dgu[m * 2 * I + I + i] = st16<kF16>(e.du);
-            dw += e.dw;
+    for (int i0 = threadIdx.x; i0 < I; i0 += 256 * kAhead) {
+        uint16_t g[kAhead], u[kAhead], d[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + 256 * j;
+            if (i >= I) continue;
+            g[j] = ld_after(gr + i);
+            u[j] = ld_after(ur + i);
+            if (kGrad) d[j] = ld_after(dr + i);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + 256 * j;
+            if (i >= I) continue;
+            const Elem e = element<kGrad>(ld16<kF16>(g[j]), ld16<kF16>(u[j]), w, kGrad ? ld16<kF16>(d[j]) : 0.0f);
+            if (!kGrad) {
+                a.h[m * I + i] = st16<kF16>(e.h);
+            } else {
+                a.dgu[m * 2 * I + i] = st16<kF16>(e.dg);
+                a.dgu[m * 2 * I + I + i] = st16<kF16>(e.du);
+                dw += e.dw;
+            }
         }
     }
     if (kGrad && a.dw) {
