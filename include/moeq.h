@@ -471,11 +471,12 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  * W: one matrix (n = 1) of either affine format, any `out`, group a multiple of 32 that divides
  * `in`, packed words 16-byte aligned; in <= MOEQ_MAX_WIDTH, out <= 1 << 24 and T <= MOEQ_MAX_ROWS, or
  * MOE_ERR_UNSUPPORTED.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
- * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  With few rows (16, or a few times as many for
- * small matrices) the codes enter the sums as whole numbers, s and b once per group, and x is exact down to 2^-27
- * of the largest of its 32 or 64 neighbours, off by at most 2^-35 of that below; larger T, and every
- * dx, first writes the matrix into the workspace as bf16 (one rounding per weight, at most 2^-8 of it)
- * and multiplies that.  An infinite
+ * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  Up to 16 rows
+ * (of 8-bit codes up to 52,000 inputs), and up to 16384 rows of matrices so small that it is the faster way (64 x 2048
+ * up to 2016 rows, 2048 x 2048 up to 80), the codes enter the sums as whole numbers, s and b once per group, and x is
+ * exact down to 2^-27 of the largest of its 32 or 64 neighbours, off by at most 2^-35 of that below: so it is wherever
+ * the size function says 256 bytes.  Other calls, and every dx, first write the matrix into the workspace as bf16 (one
+ * rounding per weight, at most 2^-8 of it) and multiply that.  An infinite
  * or NaN input makes the outputs that depend on it infinite or NaN.
  * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses),
  * 256-byte aligned, initialised once with moe_workspace_init (bytes that never fall with T: one for the
@@ -499,7 +500,8 @@ MOEQ_API moe_status moe_affine_linear_dx(const moe_qtensor* W, const uint16_t* d
  *  moe_grouped_matmul_dx: dx[m][k]    = sum_n dy[m][n] W[g][n][k]     dy [M][N], dx [M][K]
  *  moe_grouped_matmul_dw: dw[g][n][k] = sum_m dy[m][n] x[m][k]        dw [G][N][K]
  * All pointers device memory.  dtype: MOE_DT_BF16 or MOE_DT_F16, of x, dy, W and the output; dw may
- * also be MOE_DT_F32 (out_dtype).  fp32 accumulation, one rounding at the end.  accumulate = 1: dw
+ * also be MOE_DT_F32 (out_dtype).  fp32 accumulation, one rounding at the end; the tensor core's additions round
+ * toward zero, over 8192 terms at most (512 for fp32 results), and longer sums are added up in rounded parts.  accumulate = 1: dw
  * holds earlier gradients and the sums are added to them (in fp32, rounded once); 0: dw is
  * overwritten, with zeros for a group without rows.
  *  offsets device int32 [G+1], non-decreasing within [0, M]; NULL with G = 1: one group of all M
@@ -532,7 +534,7 @@ MOEQ_API moe_status moe_grouped_matmul_dw(int32_t dtype, const void* dy, const v
  * (SiLU on the gate branch, as in moe_ffn_forward.)  dtype: MOE_DT_BF16 or MOE_DT_F16, of gu, h, dh
  * and dgu; w, dw fp32 [M]; w NULL: 1; dw NULL: not wanted.  Rows [offsets[0], offsets[G]) of the
  * G + 1 offsets on the device (clamped to [0, M]); offsets NULL: all M.  Other rows are neither read
- * nor written.  fp32 arithmetic, one rounding.  I <= MOEQ_MAX_WIDTH, M <= MOEQ_MAX_ROWS.  Outputs may not alias inputs. */
+ * nor written.  fp32 arithmetic (sigmoid off by up to (10 + 1.5 |gate|) 2^-24 of itself), one rounding.  I <= MOEQ_MAX_WIDTH, M <= MOEQ_MAX_ROWS.  Outputs may not alias inputs. */
 MOEQ_API moe_status moe_swiglu(int32_t dtype, const void* gu, const float* w, const int32_t* offsets, int32_t G,
                                int32_t M, int32_t I, void* h, moe_stream stream);
 MOEQ_API moe_status moe_swiglu_grad(int32_t dtype, const void* gu, const float* w, const void* dh,

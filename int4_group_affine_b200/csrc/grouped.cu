@@ -15,8 +15,8 @@
 //
 // Bound by the instructions that fetch, shift and place the operands (a step of a lone block takes 2500
 // cycles: copies 500 to 800, shifting 1000 to 1400, products 800) and by the warp-level tensor path
-// (about a quarter of tcgen05's rate): 8000 rows on experts of 1003 to 1001, forward 144 us (112 TFLOP/s;
-// with 2-byte loads into 64 x 64 tiles 369), weight gradient 137, to fp32 160.
+// (about a quarter of tcgen05's rate): 7500 rows on 16 experts of 1003 to 1001, forward 145 us (104 TFLOP/s;
+// with 2-byte loads into 64 x 64 tiles 369), row gradient 135, weight gradient 129, to fp32 157.
 #include <cuda_fp16.h>
 
 #include "grouped.cuh"

@@ -41,7 +41,8 @@
 // of two, up to three a step, the row gradient below took 76 us).  Whole calls: many small groups run
 // at the speed of the memory (16,380 rows on 256 experts of 1024 x 2048: 177 us, 6.6 TB/s), large ones
 // at the tensor cores' and the power limit (16384 rows on 16 experts, row gradient: 68 us), the fp32
-// weight gradient at its stores (64 x 1024 x 2048: 135 us, 97 for the stores alone, 93 without them).
+// weight gradient at its stores and loads, which overlap in part (64 x 1024 x 2048: 124 to 147 us, 97 for the
+// stores alone, 93 without them).
 //
 // Long sums: the tensor core's accumulation rounds toward zero, an error that grows with the sum's
 // length (measured 4.7e-7 of the result at 512 terms, 9.1e-6 at 8192; 4.5e-4 at 65536 of one sign, as
