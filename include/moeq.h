@@ -475,7 +475,7 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  * (of 8-bit codes up to 52,000 inputs), and up to 16384 rows of matrices so small that it is the faster way (64 x 2048
  * up to 2016 rows, 2048 x 2048 up to 80), the codes enter the sums as whole numbers, s and b once per group, and x is
  * exact down to 2^-27 of the largest of its 32 or 64 neighbours, off by at most 2^-35 of that below: so it is wherever
- * the size function says 256 bytes.  Other calls, and every dx, first write the matrix into the workspace as bf16 (one
+ * the size function says 256 bytes (the sum of 64 x has to be an fp32 number: any x below 2^122).  Other calls, and every dx, first write the matrix into the workspace as bf16 (one
  * rounding per weight, at most 2^-8 of it) and multiply that.  An infinite
  * or NaN input makes the outputs that depend on it infinite or NaN.
  * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses),
