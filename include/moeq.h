@@ -469,19 +469,21 @@ MOEQ_API moe_status moe_mixed_mlp_forward_a8(const moe_mixed_tensor* gate, const
  *  moe_affine_linear_dx: dx[t][k] = sum_n dy[t][n] (s q + b)[n][k], the gradient of x through
  *    the frozen packed weights (adapter training over the int4 base, section 二 of that page).
  * W: one matrix (n = 1) of either affine format, any `out`, group a multiple of 32 that divides
- * `in`, packed words 16-byte aligned; in <= MOEQ_MAX_WIDTH, out <= 1 << 24 and T <= MOEQ_MAX_ROWS, or
- * MOE_ERR_UNSUPPORTED.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out], dy 16-byte aligned
- * when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.  Up to 16 rows
- * (of 8-bit codes up to 52,000 inputs), and up to 16384 rows of matrices so small that it is the faster way (64 x 2048
- * up to 2016 rows, 2048 x 2048 up to 80), the codes enter the sums as whole numbers, s and b once per group, and x is
- * exact down to 2^-27 of the largest of its 32 or 64 neighbours, off by at most 2^-35 of that below: so it is wherever
- * the size function says 256 bytes (the sum of 64 x has to be an fp32 number: any x below 2^122).  Other calls, and every dx, first write the matrix into the workspace as bf16 (one
- * rounding per weight, at most 2^-8 of it) and multiply that.  An infinite
- * or NaN input makes the outputs that depend on it infinite or NaN.
- * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses),
- * 256-byte aligned, initialised once with moe_workspace_init (bytes that never fall with T: one for the
- * largest T serves fewer rows); it holds the status word, and nothing else outlives a call, but calls that may run at the same time (two streams, two graphs'
- * replays) each need their own.  T = 0 enqueues nothing. */
+ * `in`, packed words 16-byte aligned; in <= MOEQ_MAX_WIDTH, out <= 1 << 24 and T <= MOEQ_MAX_ROWS,
+ * or MOE_ERR_UNSUPPORTED.  x, dx device bf16 [T][in], 16-byte aligned; y, dy device bf16 [T][out],
+ * dy 16-byte aligned when out is a multiple of 8; outputs may not alias inputs.  fp32 accumulation.
+ * Up to 16 rows (of 8-bit codes up to 52,000 inputs), and up to 16384 rows of matrices so small that
+ * it is the faster way (64 x 2048 up to 2016 rows, 2048 x 2048 up to 80), the codes enter the sums as
+ * whole numbers, s and b once per group, and x is exact down to 2^-27 of the largest of its 32 or 64
+ * neighbours, off by at most 2^-35 of that below (and below 2^122, so that their sum is an fp32
+ * number): so it is wherever the size function says 256 bytes.  Other calls, and every dx, first write
+ * the matrix into the workspace as bf16 (one rounding per weight, at most 2^-8 of it) and multiply
+ * that.  An infinite or NaN input makes the outputs that depend on it infinite or NaN.
+ * Workspace: the size function's bytes for this W and T (0 for arguments the call refuses), which never
+ * fall with T, so that one for the largest T serves fewer rows; 256-byte aligned, initialised once with
+ * moe_workspace_init.  It holds the status word, and nothing else outlives a call, but calls that may
+ * run at the same time (two streams, two graphs' replays) each need their own.  T = 0 enqueues
+ * nothing. */
 MOEQ_API size_t moe_affine_linear_workspace_bytes(const moe_qtensor* W, int32_t T);
 MOEQ_API moe_status moe_affine_linear(const moe_qtensor* W, const uint16_t* x, int32_t T, uint16_t* y,
                                       void* workspace, size_t ws_bytes, moe_stream stream);
